@@ -29,6 +29,12 @@ NVQ_PATH_GEMV = 0
 NVQ_PATH_GEMM = 1
 NVQ_PATH_GEMV_DOT4 = 2
 NVQ_GEMV_MAX_M = 15
+NVQ_TYPE_F32 = 0
+NVQ_TYPE_F16 = 1
+NVQ_TYPE_BF16 = 2
+NVQ_KV_Q8_0 = 0
+NVQ_KV_F16 = 1
+NVQ_KV_BF16 = 2
 
 # Every symbol include/nvq.h and include/nvq_probe.h declare.
 EXPORTS = (
@@ -41,6 +47,7 @@ EXPORTS = (
     "nvq_debug_isums_iq4_xs",
     "nvq_q5_k_weight_bytes", "nvq_q6_k_weight_bytes", "nvq_pack_q5_k", "nvq_pack_q6_k",
     "nvq_gemv_q5_k", "nvq_gemm_q5_k", "nvq_gemv_q6_k", "nvq_gemm_q6_k",
+    "nvq_kv_write", "nvq_kv_read", "nvq_attn_decode_workspace_bytes", "nvq_attn_decode", "nvq_attn_prompt",
     "nvq_status_str", "nvq_last_error",
     "nvq_probe_read", "nvq_probe_gemv_loads", "nvq_probe_mfma",
 )
@@ -104,6 +111,15 @@ def lib() -> ctypes.CDLL:
             "nvq_gemm_q5_k": (ctypes.c_int, [P, P, P, P, I64, I64, I64, P, P, SZ, P]),
             "nvq_gemv_q6_k": (ctypes.c_int, [P, P, P, I64, I64, I64, P, P]),
             "nvq_gemm_q6_k": (ctypes.c_int, [P, P, P, I64, I64, I64, P, P, SZ, P]),
+            "nvq_kv_write": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, P, I64, I64, P, I64, I64, P, I64, I64, I64,
+                                            P, P, P, P, I64, I64, P]),
+            "nvq_kv_read": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, P, I64, I64, P, I64, I64, P, I64, I64, I64,
+                                           P, P, P, P, I64, I64, P]),
+            "nvq_attn_decode_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I64]),
+            "nvq_attn_decode": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, P, I64, I64, I64, I64, I64, I64, P, P, P, P,
+                                               I64, I64, P, I64, P, F, P, P, SZ, P]),
+            "nvq_attn_prompt": (ctypes.c_int, [ctypes.c_int, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, F,
+                                               ctypes.c_int, P]),
             "nvq_probe_read": (ctypes.c_int, [P, SZ, ctypes.c_int, P, P]),
             "nvq_probe_gemv_loads": (ctypes.c_int, [P, I64, I64, ctypes.c_int, ctypes.c_int, ctypes.c_int, P, P]),
             "nvq_probe_mfma": (ctypes.c_int, [ctypes.c_int, I64, ctypes.c_int, P, P]),
@@ -601,6 +617,149 @@ def nvq_debug_isums(fmt: int, path: int, w, q, N: int, isums, stream=None) -> No
     _weights(w, nbytes, "w")
     _check(lib().nvq_debug_isums(int(fmt), int(path), _ptr(w), _ptr(q), M, N, K, _ptr(isums),
                                  _stream(stream, q)), "nvq_debug_isums")
+
+
+# ---------------------------------------------------------------------------
+# paged key-value cache and attention
+# ---------------------------------------------------------------------------
+
+def _row_type(t, name):
+    """NVQ_TYPE_* of a row tensor [rows, heads, D] whose channels are contiguous; other strides are passed on."""
+    import torch
+
+    if t is None or t.dim() != 3:
+        raise ValueError(f"{name}: a tensor [rows, heads, D] is required")
+    code = {torch.float32: NVQ_TYPE_F32, torch.float16: NVQ_TYPE_F16, torch.bfloat16: NVQ_TYPE_BF16}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected float32, float16 or bfloat16")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: a row's channels must be contiguous")
+    return code
+
+
+def _same_device(*tensors):
+    """Every tensor on the current GPU: pointers of another one must not reach a launch on this one's stream."""
+    import torch
+
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != here):
+            raise ValueError(f"tensor on {t.device}, expected the current device cuda:{here}")
+
+
+def _kv_cache(k_cache, v_cache, k_d, v_d):
+    """(format, n_pages, heads, page, D) of a cache [n_pages, heads, page, D]."""
+    import torch
+
+    if k_cache is None or k_cache.dim() != 4:
+        raise ValueError("k_cache: a tensor [n_pages, heads, page, D] is required")
+    fmt = {torch.int8: NVQ_KV_Q8_0, torch.float16: NVQ_KV_F16, torch.bfloat16: NVQ_KV_BF16}.get(k_cache.dtype)
+    if fmt is None:
+        raise ValueError(f"k_cache: dtype {k_cache.dtype}, expected int8 (Q8_0), float16 or bfloat16")
+    _need(v_cache, k_cache.dtype, k_cache.shape, "v_cache")
+    n_pages, heads, page, D = k_cache.shape
+    for t, name in ((k_d, "k_d"), (v_d, "v_d")):
+        if fmt != NVQ_KV_Q8_0:
+            if t is not None:
+                raise ValueError(f"{name}: a 16-bit cache has no scales")
+        elif t is None or tuple(t.shape) != (n_pages, heads, page, D // 32) or t.element_size() != 2:
+            raise ValueError(f"{name} must be a 2-byte tensor [n_pages, heads, page, D/32]")
+    return fmt, n_pages, heads, page, D
+
+
+def _kv_copy(name, k, v, slots, k_cache, v_cache, k_d, v_d, stream):
+    import torch
+
+    fmt, n_pages, heads, page, D = _kv_cache(k_cache, v_cache, k_d, v_d)
+    code = _row_type(k, "k")
+    T = k.shape[0]
+    _need(k, k.dtype, (T, heads, D), "k")
+    _need(v, k.dtype, (T, heads, D), "v")
+    _row_type(v, "v")
+    _need(slots, torch.int64, (T,), "slots")
+    _same_device(k, v, slots, k_cache, v_cache, k_d, v_d)
+    _check(getattr(lib(), name)(fmt, code, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
+                                _ptr(slots), T, heads, D, _ptr(k_cache), _ptr(v_cache), _ptr(k_d), _ptr(v_d), n_pages,
+                                page, _stream(stream, k_cache)), name)
+
+
+def nvq_kv_write(k, v, slots, k_cache, v_cache, k_d=None, v_d=None, stream=None) -> None:
+    """Rows k, v [T, Hkv, D] (float32, float16 or bfloat16; token and head strides free) into a paged cache
+    [n_pages, Hkv, page, D] at slots int64 [T] (page number * page + place; negative: none).  An int8 cache is
+    Q8_0 and takes the binary16 scales k_d, v_d [n_pages, Hkv, page, D/32]; a 16-bit one takes none."""
+    _kv_copy("nvq_kv_write", k, v, slots, k_cache, v_cache, k_d, v_d, stream)
+
+
+def nvq_kv_read(k_cache, v_cache, slots, k, v, k_d=None, v_d=None, stream=None) -> None:
+    """The cache rows at slots int64 [T] into k, v [T, Hkv, D] (arguments as nvq_kv_write's)."""
+    _kv_copy("nvq_kv_read", k, v, slots, k_cache, v_cache, k_d, v_d, stream)
+
+
+def nvq_attn_decode_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, max_pages: int, page: int) -> int:
+    return int(lib().nvq_attn_decode_workspace_bytes(B, Hq, Hkv, D, max_pages, page))
+
+
+def nvq_attn_decode(q, k_cache, v_cache, table, lengths, out, k_d=None, v_d=None, scale=None, workspace=None,
+                    stream=None) -> None:
+    """One new token per sequence: q [B, Hq, D] (strides free), the paged cache, table int32 [B, max_pages] and
+    lengths int32 [B] -> out [B, Hq, D] of q's type.  scale: 1 / sqrt(D) unless given."""
+    import torch
+
+    fmt, n_pages, heads, page, D = _kv_cache(k_cache, v_cache, k_d, v_d)
+    code = _row_type(q, "q")
+    B, Hq = q.shape[:2]
+    _need(q, q.dtype, (B, Hq, D), "q")
+    _need(out, q.dtype, (B, Hq, D), "out")
+    if table is None or table.dim() != 2:
+        raise ValueError("table: int32 [B, max_pages] is required")
+    max_pages = table.shape[1]
+    _need(table, torch.int32, (B, max_pages), "table")
+    _need(lengths, torch.int32, (B,), "lengths")
+    _same_device(q, k_cache, v_cache, table, lengths, out, k_d, v_d, workspace)
+    if workspace is None:
+        workspace = _workspace(nvq_attn_decode_workspace_bytes(B, Hq, heads, D, max_pages, page), stream, q)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().nvq_attn_decode(fmt, code, q.data_ptr(), q.stride(0), q.stride(1), B, Hq, heads, D, _ptr(k_cache),
+                                 _ptr(v_cache), _ptr(k_d), _ptr(v_d), n_pages, page, _ptr(table), max_pages,
+                                 _ptr(lengths), D ** -0.5 if scale is None else float(scale), _ptr(out),
+                                 _ptr(workspace), ws_bytes, _stream(stream, q)), "nvq_attn_decode")
+
+
+def _workspace(nbytes, stream, like):
+    """Scratch of one call.  torch's allocator hands it out again in the order of the stream that it was allocated
+    on, so on a stream of the caller's it has to be told of that one."""
+    import torch
+
+    if not nbytes:
+        return None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if stream is not None and int(stream) != torch.cuda.current_stream(like.device).cuda_stream:
+        ws.record_stream(torch.cuda.ExternalStream(int(stream), device=like.device))
+    return ws
+
+
+def nvq_attn_prompt(q, k, v, cu_q, cu_k, out, scale=None, causal=True, stream=None) -> None:
+    """Packed prompts: q [Tq, Hq, D], k, v [Tk, Hkv, D] (float16 or bfloat16, strides free), cu_q, cu_k int32 [B+1]
+    -> out [Tq, Hq, D] (strides free).  Query i of m sees keys j <= i + n - m of its n (causal), else all.
+    scale: 1 / sqrt(D) unless given."""
+    import torch
+
+    code = _row_type(q, "q")
+    Tq, Hq, D = q.shape
+    Tk, Hkv = k.shape[:2] if k is not None and k.dim() == 3 else (-1, -1)
+    for t, name, shape in ((k, "k", (Tk, Hkv, D)), (v, "v", (Tk, Hkv, D)), (out, "out", (Tq, Hq, D))):
+        _need(t, q.dtype, shape, name)
+        _row_type(t, name)
+    B = cu_q.shape[0] - 1 if cu_q is not None and cu_q.dim() == 1 else -1
+    if B < 0:
+        raise ValueError("cu_q: int32 [B + 1] is required")
+    _need(cu_q, torch.int32, (B + 1,), "cu_q")
+    _need(cu_k, torch.int32, (B + 1,), "cu_k")
+    _same_device(q, k, v, cu_q, cu_k, out)
+    strides = (ctypes.c_int64 * 8)(*(s for t in (q, k, v, out) for s in t.stride()[:2]))
+    _check(lib().nvq_attn_prompt(code, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), strides, _ptr(cu_q),
+                                 _ptr(cu_k), B, Tq, Tk, Hq, Hkv, D, D ** -0.5 if scale is None else float(scale),
+                                 1 if causal else 0, _stream(stream, q)), "nvq_attn_prompt")
 
 
 # ---------------------------------------------------------------------------

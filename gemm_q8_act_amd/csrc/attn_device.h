@@ -1,0 +1,163 @@
+// attn_device.h -- device helpers shared by the cache and attention kernels: element
+// types, matrix products by type, exchanges between lanes.
+#pragma once
+
+#include "nvq.h"
+#include "nvq_device.h"
+
+namespace nvq {
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+
+// The element type of a cache format's codes (Q8_0's operands are binary16).
+template <int FMT>
+struct CacheType {
+  typedef _Float16 type;
+};
+template <>
+struct CacheType<NVQ_KV_BF16> {
+  typedef __bf16 type;
+};
+
+// Two floats rounded to nearest even into one dword of 16-bit elements (one instruction), and back.
+template <typename T>
+__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+  typedef T t2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((floatx2{a, b}), t2));
+}
+template <typename T>
+__device__ __forceinline__ void unpack_pair(uint32_t v, float (&x)[2]) {
+  typedef T t2 __attribute__((ext_vector_type(2)));
+  const t2 t = __builtin_bit_cast(t2, v);
+  x[0] = (float)t[0], x[1] = (float)t[1];
+}
+
+// Two neighbouring elements of a row as floats; p is aligned to the pair.
+__device__ __forceinline__ void load_pair(const float* p, float (&x)[2]) {
+  const floatx2 t = *reinterpret_cast<const floatx2*>(p);
+  x[0] = t[0], x[1] = t[1];
+}
+template <typename T>
+__device__ __forceinline__ void load_pair(const T* p, float (&x)[2]) {
+  unpack_pair<T>(*reinterpret_cast<const uint32_t*>(p), x);
+}
+__device__ __forceinline__ void store_pair(float* p, float a, float b) { *reinterpret_cast<floatx2*>(p) = floatx2{a, b}; }
+template <typename T>
+__device__ __forceinline__ void store_pair(T* p, float a, float b) {
+  *reinterpret_cast<uint32_t*>(p) = pack_pair<T>(a, b);
+}
+
+// 8 consecutive elements of a row of element type `type` (NVQ_TYPE_*, uniform), from element
+// `at` on; 16-byte aligned.
+__device__ __forceinline__ void load_8(const void* p, int type, int64_t at, float (&x)[8]) {
+  if (type == NVQ_TYPE_F32) {
+    const floatx4* s = reinterpret_cast<const floatx4*>(reinterpret_cast<const float*>(p) + at);
+    const floatx4 a = s[0], b = s[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = a[i], x[4 + i] = b[i];
+  } else {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(p) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float t[2];
+      if (type == NVQ_TYPE_F16)
+        unpack_pair<_Float16>(w[i], t);
+      else
+        unpack_pair<__bf16>(w[i], t);
+      x[2 * i] = t[0], x[2 * i + 1] = t[1];
+    }
+  }
+}
+__device__ __forceinline__ void store_1(void* p, int type, int64_t at, float x) {
+  if (type == NVQ_TYPE_F32)
+    reinterpret_cast<float*>(p)[at] = x;
+  else if (type == NVQ_TYPE_F16)
+    reinterpret_cast<_Float16*>(p)[at] = (_Float16)x;
+  else
+    reinterpret_cast<__bf16*>(p)[at] = (__bf16)x;
+}
+// N (even) consecutive elements from element `at` on; `at` is a multiple of N or of 8.
+template <int N>
+__device__ __forceinline__ void store_n(void* p, int type, int64_t at, const float (&x)[N]) {
+  if (type == NVQ_TYPE_F32) {
+    float* d = reinterpret_cast<float*>(p) + at;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) *reinterpret_cast<floatx2*>(d + i) = floatx2{x[i], x[i + 1]};
+  } else {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      w[i] = type == NVQ_TYPE_F16 ? pack_pair<_Float16>(x[2 * i], x[2 * i + 1]) : pack_pair<__bf16>(x[2 * i], x[2 * i + 1]);
+    uint32_t* d = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p) + at);
+    if constexpr (N % 8 == 0) {
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i) reinterpret_cast<u32x4*>(d)[i] = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) d[i] = w[i];
+    }
+  }
+}
+
+// An operand of four dwords, and the two matrix products of the 16-bit types.
+struct Frag {
+  uint32_t v[4];
+};
+template <typename T>
+__device__ __forceinline__ floatx4 mfma16(const Frag& a, const Frag& b, floatx4 c) {
+  const u32x4 x = {a.v[0], a.v[1], a.v[2], a.v[3]}, y = {b.v[0], b.v[1], b.v[2], b.v[3]};
+  if constexpr (__is_same(T, _Float16))
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, x), __builtin_bit_cast(half8_t, y), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x), __builtin_bit_cast(bf16x8_t, y), c, 0, 0, 0);
+}
+template <typename T>
+__device__ __forceinline__ floatx16 mfma32(const Frag& a, const Frag& b, floatx16 c) {
+  const u32x4 x = {a.v[0], a.v[1], a.v[2], a.v[3]}, y = {b.v[0], b.v[1], b.v[2], b.v[3]};
+  if constexpr (__is_same(T, _Float16))
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, x), __builtin_bit_cast(half8_t, y), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, x), __builtin_bit_cast(bf16x8_t, y), c, 0, 0, 0);
+}
+
+// 2^x (v_exp_f32: about one unit in the last place; results below the normal range are 0)
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Largest and sum over the lanes 32 apart, 16 apart: the instruction swaps halves of two
+// registers.  (The results go into scalars first: a bit cast of a vector's element reads
+// element 0.)
+struct Halves {
+  float a, b;
+};
+__device__ __forceinline__ Halves halves_32(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t a = r[0], b = r[1];
+  return {__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+__device__ __forceinline__ Halves halves_16(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t a = r[0], b = r[1];
+  return {__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+__device__ __forceinline__ float max_32(float x) {
+  const Halves h = halves_32(x);
+  return fmaxf(h.a, h.b);
+}
+__device__ __forceinline__ float sum_32(float x) {
+  const Halves h = halves_32(x);
+  return h.a + h.b;
+}
+__device__ __forceinline__ float max_16(float x) {
+  const Halves h = halves_16(x);
+  return fmaxf(h.a, h.b);
+}
+__device__ __forceinline__ float sum_16(float x) {
+  const Halves h = halves_16(x);
+  return h.a + h.b;
+}
+
+}  // namespace nvq

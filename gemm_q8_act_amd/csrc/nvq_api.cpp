@@ -625,6 +625,155 @@ nvq_status nvq_debug_isums(int fmt, int path, const void* w, const int8_t* q, in
   return NVQ_OK;
 }
 
+// ---- paged key-value cache and attention ----
+
+namespace {
+
+size_t type_bytes(int type) { return type == NVQ_TYPE_F32 ? 4 : 2; }
+
+// A row argument [T][H][D]: every row starts at a multiple of 16 bytes.  The stride of a
+// dimension of one has no meaning.
+nvq_status check_rows(const char* who, const char* name, const void* p, int type, int64_t T, int64_t H, int64_t stride_t,
+                      int64_t stride_h) {
+  if (T <= 1) stride_t = 0;
+  if (H <= 1) stride_h = 0;
+  if (stride_t < 0 || stride_h < 0 || stride_t >= kMaxElems || stride_h >= kMaxElems)
+    return fail(NVQ_ERR_SHAPE, "%s: strides of %s out of range", who, name);
+  if (!aligned(p, 16) || stride_t * (int64_t)type_bytes(type) % 16 != 0 || stride_h * (int64_t)type_bytes(type) % 16 != 0)
+    return fail(NVQ_ERR_ALIGN, "%s: every row of %s must start at a multiple of 16 bytes", who, name);
+  return NVQ_OK;
+}
+
+// Rows that are written must not lie on one another.
+nvq_status check_apart(const char* who, const char* name, int64_t T, int64_t H, int64_t D, int64_t stride_t, int64_t stride_h) {
+  const bool heads_inside = H == 1 || (stride_h >= D && (T == 1 || stride_t >= (H - 1) * stride_h + D));
+  const bool tokens_inside = T == 1 || (stride_t >= D && (H == 1 || stride_h >= (T - 1) * stride_t + D));
+  if (!heads_inside && !tokens_inside) return fail(NVQ_ERR_SHAPE, "%s: rows of %s overlap", who, name);
+  return NVQ_OK;
+}
+
+nvq_status check_head(const char* who, int64_t Hkv, int64_t D) {
+  if (D < 32 || D > 256 || D % 32 != 0) return fail(NVQ_ERR_SHAPE, "%s: D=%lld must be a multiple of 32 in 32 .. 256", who, (long long)D);
+  if (Hkv < 1 || Hkv > 65536) return fail(NVQ_ERR_SHAPE, "%s: Hkv=%lld outside [1, 65536]", who, (long long)Hkv);
+  return NVQ_OK;
+}
+
+bool page_ok(int64_t page) { return page >= 16 && page <= 65536 && (page & (page - 1)) == 0; }
+
+nvq_status check_cache(const char* who, int fmt, const void* k, const void* v, const void* k_d, const void* v_d, int64_t Hkv,
+                       int64_t D, int64_t n_pages, int64_t page, nvq::KvCache& c) {
+  if (fmt != NVQ_KV_Q8_0 && fmt != NVQ_KV_F16 && fmt != NVQ_KV_BF16) return fail(NVQ_ERR_RANGE, "%s: fmt=%d is not NVQ_KV_*", who, fmt);
+  NVQ_TRY(check_head(who, Hkv, D));
+  if (!k || !v || (fmt == NVQ_KV_Q8_0 && (!k_d || !v_d))) return fail(NVQ_ERR_NULL, "%s: NULL cache pointer", who);
+  if (fmt != NVQ_KV_Q8_0 && (k_d || v_d)) return fail(NVQ_ERR_RANGE, "%s: a 16-bit cache has no scales", who);
+  if (!page_ok(page)) return fail(NVQ_ERR_SHAPE, "%s: page=%lld must be a power of two in 16 .. 65536", who, (long long)page);
+  if (n_pages < 1 || n_pages >= kMaxDim || n_pages * page > kMaxElems / Hkv)
+    return fail(NVQ_ERR_SHAPE, "%s: n_pages=%lld out of range", who, (long long)n_pages);
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_d, 16) || !aligned(v_d, 16))
+    return fail(NVQ_ERR_ALIGN, "%s: cache pointers must be 16-byte aligned", who);
+  c = {k, v, k_d, v_d, n_pages, __builtin_ctzll((unsigned long long)page)};
+  return NVQ_OK;
+}
+
+nvq_status kv_copy(bool write, const char* who, int fmt, int type, const void* k, int64_t k_st, int64_t k_sh, const void* v,
+                   int64_t v_st, int64_t v_sh, const int64_t* slots, int64_t T, int64_t Hkv, int64_t D, const void* k_cache,
+                   const void* v_cache, const void* k_d, const void* v_d, int64_t n_pages, int64_t page, void* stream) {
+  if (type < NVQ_TYPE_F32 || type > NVQ_TYPE_BF16) return fail(NVQ_ERR_RANGE, "%s: type=%d is not NVQ_TYPE_*", who, type);
+  nvq::KvCache c;
+  NVQ_TRY(check_cache(who, fmt, k_cache, v_cache, k_d, v_d, Hkv, D, n_pages, page, c));
+  if (T < 0 || T >= (int64_t(1) << 34) / Hkv) return fail(NVQ_ERR_SHAPE, "%s: T=%lld out of range", who, (long long)T);
+  if (T == 0) return NVQ_OK;
+  if (!k || !v || !slots) return fail(NVQ_ERR_NULL, "%s: NULL pointer", who);
+  NVQ_TRY(check_rows(who, "k", k, type, T, Hkv, k_st, k_sh));
+  NVQ_TRY(check_rows(who, "v", v, type, T, Hkv, v_st, v_sh));
+  if (!write) {
+    NVQ_TRY(check_apart(who, "k", T, Hkv, D, k_st, k_sh));
+    NVQ_TRY(check_apart(who, "v", T, Hkv, D, v_st, v_sh));
+  }
+  if (!aligned(slots, 8)) return fail(NVQ_ERR_ALIGN, "%s: slots must be 8-byte aligned", who);
+  NVQ_TRY(check_device());
+  const int64_t strides[4] = {k_st, k_sh, v_st, v_sh};
+  return launched(nvq::launch_kv_copy(write, fmt, type, k, v, strides, slots, T, Hkv, D, c, (hipStream_t)stream), who);
+}
+
+}  // namespace
+
+nvq_status nvq_kv_write(int fmt, int type, const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v,
+                        int64_t v_stride_t, int64_t v_stride_h, const int64_t* slots, int64_t T, int64_t Hkv, int64_t D,
+                        void* k_cache, void* v_cache, uint16_t* k_d, uint16_t* v_d, int64_t n_pages, int64_t page,
+                        void* stream) {
+  return kv_copy(true, "nvq_kv_write", fmt, type, k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, slots, T, Hkv, D,
+                 k_cache, v_cache, k_d, v_d, n_pages, page, stream);
+}
+
+nvq_status nvq_kv_read(int fmt, int type, void* k, int64_t k_stride_t, int64_t k_stride_h, void* v, int64_t v_stride_t,
+                       int64_t v_stride_h, const int64_t* slots, int64_t T, int64_t Hkv, int64_t D, const void* k_cache,
+                       const void* v_cache, const uint16_t* k_d, const uint16_t* v_d, int64_t n_pages, int64_t page,
+                       void* stream) {
+  return kv_copy(false, "nvq_kv_read", fmt, type, k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, slots, T, Hkv, D,
+                 k_cache, v_cache, k_d, v_d, n_pages, page, stream);
+}
+
+// One new token per sequence: the capacity in keys of all sequences has to fit an int.
+static bool decode_shape_ok(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages, int64_t page) {
+  return B >= 1 && B < kMaxDim && Hkv >= 1 && Hkv <= 65536 && Hq >= Hkv && Hq <= 65536 && Hq % Hkv == 0 && D >= 32 && D <= 256 &&
+         D % 32 == 0 && page_ok(page) && max_pages >= 1 && max_pages < kMaxDim / page && B < kMaxDim / (max_pages * page) &&
+         nvq::attn_decode_groups(B, Hq, Hkv, max_pages * page) < kMaxDim;
+}
+
+size_t nvq_attn_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages, int64_t page) {
+  if (!decode_shape_ok(B, Hq, Hkv, D, max_pages, page)) return 0;
+  return nvq::attn_decode_workspace(B, Hq, Hkv, D, max_pages * page);
+}
+
+nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b, int64_t q_stride_h, int64_t B, int64_t Hq,
+                           int64_t Hkv, int64_t D, const void* k_cache, const void* v_cache, const uint16_t* k_d,
+                           const uint16_t* v_d, int64_t n_pages, int64_t page, const int32_t* table, int64_t max_pages,
+                           const int32_t* lengths, float scale, void* out, void* workspace, size_t ws_bytes, void* stream) {
+  const char* who = "nvq_attn_decode";
+  if (type < NVQ_TYPE_F32 || type > NVQ_TYPE_BF16) return fail(NVQ_ERR_RANGE, "%s: type=%d is not NVQ_TYPE_*", who, type);
+  nvq::KvCache c;
+  NVQ_TRY(check_cache(who, fmt, k_cache, v_cache, k_d, v_d, Hkv, D, n_pages, page, c));
+  if (B == 0) return NVQ_OK;
+  if (!decode_shape_ok(B, Hq, Hkv, D, max_pages, page))
+    return fail(NVQ_ERR_SHAPE, "%s: B=%lld, Hq=%lld, Hkv=%lld, max_pages=%lld, page=%lld out of range (Hq a multiple of Hkv, B * max_pages * page < 2^31)",
+                who, (long long)B, (long long)Hq, (long long)Hkv, (long long)max_pages, (long long)page);
+  if (!q || !table || !lengths || !out) return fail(NVQ_ERR_NULL, "%s: NULL pointer", who);
+  NVQ_TRY(check_rows(who, "q", q, type, B, Hq, q_stride_b, q_stride_h));
+  if (!aligned(out, 16) || !aligned(table, 4) || !aligned(lengths, 4))
+    return fail(NVQ_ERR_ALIGN, "%s: out must be 16-byte aligned, table and lengths 4-byte", who);
+  const size_t need = nvq::attn_decode_workspace(B, Hq, Hkv, D, max_pages * page);
+  if (need > 0 && (!workspace || ws_bytes < need)) return fail(NVQ_ERR_WORKSPACE, "%s: workspace of %zu bytes required, got %zu", who, need, workspace ? ws_bytes : (size_t)0);
+  if (need > 0 && !aligned(workspace, 16)) return fail(NVQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", who);
+  NVQ_TRY(check_device());
+  return launched(nvq::launch_attn_decode(fmt, type, q, q_stride_b, q_stride_h, B, Hq, Hkv, D, c, table, max_pages, lengths, scale, out,
+                                          workspace, (hipStream_t)stream), who);
+}
+
+nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v, void* out, const int64_t* strides,
+                           const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,
+                           int64_t Hkv, int64_t D, float scale, int causal, void* stream) {
+  const char* who = "nvq_attn_prompt";
+  if (type != NVQ_TYPE_F16 && type != NVQ_TYPE_BF16) return fail(NVQ_ERR_RANGE, "%s: type=%d must be NVQ_TYPE_F16 or NVQ_TYPE_BF16", who, type);
+  NVQ_TRY(check_head(who, Hkv, D));
+  if (Hq < Hkv || Hq > 65536 || Hq % Hkv != 0) return fail(NVQ_ERR_SHAPE, "%s: Hq=%lld must be a multiple of Hkv=%lld", who, (long long)Hq, (long long)Hkv);
+  constexpr int64_t most = int64_t(1) << 30;
+  if (B < 0 || B >= most || Tq < 0 || Tq >= most || Tk < 0 || Tk >= most)
+    return fail(NVQ_ERR_SHAPE, "%s: B=%lld, Tq=%lld, Tk=%lld out of range", who, (long long)B, (long long)Tq, (long long)Tk);
+  if (B == 0 || Tq == 0) return NVQ_OK;
+  if (!q || !out || !strides || !cu_q || !cu_k || (Tk > 0 && (!k || !v))) return fail(NVQ_ERR_NULL, "%s: NULL pointer", who);
+  NVQ_TRY(check_rows(who, "q", q, type, Tq, Hq, strides[0], strides[1]));
+  NVQ_TRY(check_rows(who, "k", k, type, Tk, Hkv, strides[2], strides[3]));
+  NVQ_TRY(check_rows(who, "v", v, type, Tk, Hkv, strides[4], strides[5]));
+  NVQ_TRY(check_rows(who, "out", out, type, Tq, Hq, strides[6], strides[7]));
+  NVQ_TRY(check_apart(who, "out", Tq, Hq, D, strides[6], strides[7]));
+  if (!aligned(cu_q, 4) || !aligned(cu_k, 4)) return fail(NVQ_ERR_ALIGN, "%s: cu_q and cu_k must be 4-byte aligned", who);
+  if (nvq::attn_prompt_groups(B, Tq, Hq) >= kMaxDim) return fail(NVQ_ERR_SHAPE, "%s: too many query tiles", who);
+  NVQ_TRY(check_device());
+  return launched(nvq::launch_attn_prompt(type, q, k, v, out, strides, cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, scale, causal ? 1 : 0,
+                                          (hipStream_t)stream), who);
+}
+
 // ---- measurement probes (include/nvq_probe.h) ----
 
 nvq_status nvq_probe_read(const void* src, size_t bytes, int blocks, uint32_t* sink, void* stream) {

@@ -104,6 +104,36 @@ hipError_t launch_gemv_q6_k(const uint8_t* w, const int8_t* q, const uint16_t* d
 hipError_t launch_gemm_q6_k(const uint8_t* w, const int8_t* q, const uint16_t* d16, int64_t M, int64_t N,
                             int64_t K, float* y, int32_t* isums, float* workspace, hipStream_t stream);
 
+// The paged key-value cache.  k, v: rows [n_pages][heads][page][D] of int8 codes (in the order
+// nvq.h gives) or 16-bit elements; k_d, v_d: binary16 scales [..][page][D/32] (Q8_0, else
+// null).  page = 1 << page_shift >= 16.
+struct KvCache {
+  const void* k;
+  const void* v;
+  const void* k_d;
+  const void* v_d;
+  int64_t n_pages;
+  int page_shift;
+};
+// Rows [T][heads][D] of `type` into the cache (write) or out of it; strides: k's token and
+// head stride, v's, in elements.
+hipError_t launch_kv_copy(bool write, int fmt, int type, const void* k, const void* v, const int64_t strides[4],
+                          const int64_t* slots, int64_t T, int64_t heads, int64_t D, const KvCache& c, hipStream_t stream);
+// Attention of one token per sequence over the cache (attn_decode.hip); groups: its workgroups.
+hipError_t launch_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b, int64_t q_stride_h, int64_t B,
+                              int64_t Hq, int64_t Hkv, int64_t D, const KvCache& c, const int32_t* table,
+                              int64_t table_stride, const int32_t* lengths, float scale, void* out, void* workspace,
+                              hipStream_t stream);
+size_t attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity);
+int64_t attn_decode_groups(int64_t B, int64_t Hq, int64_t Hkv, int64_t capacity);
+
+// Attention of packed prompts (attn_prompt.hip); strides: token and head stride of q, k, v
+// and out, in elements; groups: its workgroups.
+hipError_t launch_attn_prompt(int type, const void* q, const void* k, const void* v, void* out, const int64_t strides[8],
+                              const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,
+                              int64_t Hkv, int64_t D, float scale, int causal, hipStream_t stream);
+int64_t attn_prompt_groups(int64_t B, int64_t Tq, int64_t Hq);
+
 // Measurement probes (probe.hip): a streaming read of n16 16-byte units over `blocks`
 // blocks of 256 threads (sink: 4 words per block); the decode GEMV's weight loads
 // alone for waves in {4, 8, 16}, batch in {3, 5} and `splits` blocks per tile (sink:

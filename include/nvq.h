@@ -146,6 +146,14 @@ typedef int nvq_status;
 #define NVQ_FMT_IQ4_XS 3
 #define NVQ_FMT_Q5_K  4
 #define NVQ_FMT_Q6_K  5
+/* element types of query, key, value and output rows */
+#define NVQ_TYPE_F32  0
+#define NVQ_TYPE_F16  1  /* binary16 */
+#define NVQ_TYPE_BF16 2  /* bfloat16 */
+/* formats of a paged key-value cache */
+#define NVQ_KV_Q8_0 0
+#define NVQ_KV_F16  1
+#define NVQ_KV_BF16 2
 #define NVQ_PATH_GEMV      0  /* decode GEMV, matrix-core inner loop (production) */
 #define NVQ_PATH_GEMM      1  /* tiled GEMM */
 #define NVQ_PATH_GEMV_DOT4 2  /* decode GEMV, v_perm + v_dot4 inner loop (NVFP4 only) */
@@ -442,6 +450,81 @@ nvq_status nvq_gemv_iq4_xs(const void* w, const int8_t* table, const int8_t* q, 
 nvq_status nvq_gemm_iq4_xs(const void* w, const int8_t* table, const int8_t* q, const uint16_t* d_f16,
                            int64_t M, int64_t N, int64_t K, float* y, void* workspace, size_t ws_bytes,
                            void* stream);
+
+/* ---- paged key-value cache and attention ---------------------------------------- */
+
+/* What stands between the QKV product and the O product of a layer: the keys and values go
+ * into a cache (quantised to Q8_0 on the way, or kept in 16 bits), and the queries attend to
+ * it (one new token per sequence) or to the prompt's own keys and values.  The pages have
+ * no counterpart for these entries (they name the server's key-value cache without a layout);
+ * the definitions here are this library's own.
+ *
+ * Cache.  k_cache and v_cache (device) hold n_pages pages of `page` tokens for Hkv heads of
+ * D channels: rows [n_pages][Hkv][page][D].  D % 32 == 0, 32 <= D <= 256; page is a power
+ * of two in 16 .. 65536.  A token's slot is its page number * page + its place in the page.
+ *   NVQ_KV_F16, NVQ_KV_BF16: a row is D 16-bit elements in order; k_d and v_d are NULL.
+ *   NVQ_KV_Q8_0: a row is D int8 codes, and k_d / v_d hold D/32 binary16 scales a row,
+ *     [n_pages][Hkv][page][D/32]: Q8_0 of the row by the activation rule above.  The codes
+ *     of a row are interleaved over its 32-channel blocks: with nb = D/32, byte
+ *     2*nb*n + 2*b + e of a row is the code of channel 32*b + 2*n + e (n 0..15, e 0..1), so
+ *     that 1/16 of the row's bytes, in one wide access, is two channels of every block.
+ *   Rows that were never written may hold anything (they are masked, not multiplied by 0).
+ * Row arguments (q, k, v, out) are of NVQ_TYPE_F32 / F16 / BF16; their strides are in
+ * elements, a row's D channels are contiguous, every row starts at a multiple of 16 bytes.
+ * Pointers are 16-byte aligned (indexes and lengths: to their own size), NVQ_ERR_ALIGN
+ * otherwise.  T = 0 or B = 0 is NVQ_OK and enqueues nothing. */
+
+/* Rows of T tokens into the cache: k, v [T][Hkv][D] of `type` (strides between tokens and
+ * between heads), token t to slot slots[t] (device, int64).  A negative slot, or one past
+ * the cache, writes nothing.  A slot given twice in one call gets one of the two rows,
+ * or parts of both.  Q8_0: codes and scales are those of nvq_quantize_act_q8_0 on the row
+ * as float32; a 32-channel block with an infinity or NaN reads back as NaN.  16-bit
+ * formats: each element rounded once to nearest even. */
+nvq_status nvq_kv_write(int fmt, int type, const void* k, int64_t k_stride_t, int64_t k_stride_h,
+                        const void* v, int64_t v_stride_t, int64_t v_stride_h, const int64_t* slots, int64_t T,
+                        int64_t Hkv, int64_t D, void* k_cache, void* v_cache, uint16_t* k_d, uint16_t* v_d,
+                        int64_t n_pages, int64_t page, void* stream);
+
+/* The way back: k, v [T][Hkv][D] of `type` (overwritten) from the rows at slots[t]: a Q8_0
+ * element is code * scale, rounded once to the type.  A negative slot gives zeros, one past
+ * the cache NaN. */
+nvq_status nvq_kv_read(int fmt, int type, void* k, int64_t k_stride_t, int64_t k_stride_h, void* v,
+                       int64_t v_stride_t, int64_t v_stride_h, const int64_t* slots, int64_t T, int64_t Hkv,
+                       int64_t D, const void* k_cache, const void* v_cache, const uint16_t* k_d,
+                       const uint16_t* v_d, int64_t n_pages, int64_t page, void* stream);
+
+/* Attention of one new token per sequence over the cache:
+ *     out[b][h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q[b][h] . k_j),  j < lengths[b],
+ * with k_j, v_j the cache rows of key head h / (Hq/Hkv) at place j of sequence b: page
+ * table[b][j / page], place j % page.  q [B][Hq][D] of `type` (strides between sequences and
+ * between heads), out [B][Hq][D] of `type`, contiguous; table int32 [B][max_pages] and lengths
+ * int32 [B] on the device.  Hq a multiple of Hkv; B * max_pages * page < 2^31.  A sequence
+ * of length 0 gives zeros; a length outside 0 .. max_pages * page, or a page number outside the
+ * cache among its keys, gives NaN (nothing is read there).  Scores, sums and products are as
+ * exact as float32 makes them (two binary16 terms, or three bfloat16 terms, of each float
+ * operand; float32 accumulation); out is rounded once.  Non-finite values among a sequence's
+ * keys or values give non-finite results.
+ * workspace: device, at least nvq_attn_decode_workspace_bytes, contents irrelevant,
+ * overwritten; NULL when that is 0.  Calls that share it must not overlap in time. */
+size_t nvq_attn_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages, int64_t page);
+nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b, int64_t q_stride_h, int64_t B,
+                           int64_t Hq, int64_t Hkv, int64_t D, const void* k_cache, const void* v_cache,
+                           const uint16_t* k_d, const uint16_t* v_d, int64_t n_pages, int64_t page,
+                           const int32_t* table, int64_t max_pages, const int32_t* lengths, float scale, void* out,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/* Attention of whole prompts, packed one behind the other: sequence b's queries are rows
+ * cu_q[b] .. cu_q[b+1] - 1 of q [Tq][Hq][D], its keys and values rows cu_k[b] .. cu_k[b+1] - 1
+ * of k, v [Tk][Hkv][D] (int32 [B+1] on the device, ascending from 0).  With m queries and n
+ * keys, query i sees keys j <= i + n - m if causal (the last query sees all: n > m puts the
+ * queries behind n - m keys of a prefix), else all n.  A query that sees no key gives zeros.
+ * `type` NVQ_TYPE_F16 or BF16; strides[8]: token and head stride of q, k, v and out (host).
+ * Hq a multiple of Hkv; Tq, Tk < 2^30.  Rows of out in no sequence are left alone; offsets
+ * outside the tensors are cut to them.  Scores, softmax statistics and accumulation are
+ * float32; the probabilities enter the second product rounded once to `type`. */
+nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v, void* out,
+                           const int64_t* strides, const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq,
+                           int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, float scale, int causal, void* stream);
 
 /* ---- debug: integer per-16 partial sums --------------------------------------- */
 
