@@ -623,64 +623,89 @@ def nvq_debug_isums(fmt: int, path: int, w, q, N: int, isums, stream=None) -> No
 # paged key-value cache and attention
 # ---------------------------------------------------------------------------
 
-def _row_type(t, name):
-    """NVQ_TYPE_* of a row tensor [rows, heads, D] whose channels are contiguous; other strides are passed on."""
-    import torch
+# A decode step makes these calls with a few microseconds of work each, so the checks below
+# compare shapes and types directly and say more only once something is wrong.
+_row_types: dict = {}    # torch dtype -> NVQ_TYPE_*
+_cache_types: dict = {}  # torch dtype -> NVQ_KV_*
 
-    if t is None or t.dim() != 3:
-        raise ValueError(f"{name}: a tensor [rows, heads, D] is required")
-    code = {torch.float32: NVQ_TYPE_F32, torch.float16: NVQ_TYPE_F16, torch.bfloat16: NVQ_TYPE_BF16}.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected float32, float16 or bfloat16")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+
+def _attn_lib():
+    if not _row_types:
+        import torch
+
+        _row_types.update({torch.float32: NVQ_TYPE_F32, torch.float16: NVQ_TYPE_F16, torch.bfloat16: NVQ_TYPE_BF16})
+        _cache_types.update({torch.int8: NVQ_KV_Q8_0, torch.float16: NVQ_KV_F16, torch.bfloat16: NVQ_KV_BF16})
+    return _lib or lib()
+
+
+def _rows(t, dtype, shape, name):
+    """A row tensor [rows, heads, D] whose channels are contiguous (its other strides are passed on): its strides."""
+    if t is None or t.dtype != dtype or t.shape != shape:
+        _need(t, dtype, shape, name)
+    st = t.stride()
+    if st[2] != 1 and shape[2] > 1:
         raise ValueError(f"{name}: a row's channels must be contiguous")
-    return code
+    return st
 
 
-def _same_device(*tensors):
-    """Every tensor on the current GPU: pointers of another one must not reach a launch on this one's stream."""
+def _dense(t, dtype, shape, name):
+    if t is None or t.dtype != dtype or t.shape != shape:
+        _need(t, dtype, shape, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors passed to libnvq must be contiguous")
+    return t.data_ptr()
+
+
+def _row_shape(t, name):
+    if t is None or t.dim() != 3 or t.dtype not in _row_types:
+        raise ValueError(f"{name}: a float32, float16 or bfloat16 tensor [rows, heads, D] is required")
+    return t.shape
+
+
+def _on_device(stream, *tensors):
+    """Every tensor on the current GPU (pointers of another one must not reach a launch on this one's stream): the
+    stream to launch on."""
     import torch
 
     here = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != here):
+        if t is not None and t.get_device() != here:
             raise ValueError(f"tensor on {t.device}, expected the current device cuda:{here}")
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream)
 
 
 def _kv_cache(k_cache, v_cache, k_d, v_d):
-    """(format, n_pages, heads, page, D) of a cache [n_pages, heads, page, D]."""
-    import torch
-
-    if k_cache is None or k_cache.dim() != 4:
-        raise ValueError("k_cache: a tensor [n_pages, heads, page, D] is required")
-    fmt = {torch.int8: NVQ_KV_Q8_0, torch.float16: NVQ_KV_F16, torch.bfloat16: NVQ_KV_BF16}.get(k_cache.dtype)
+    """(format, shape, pointers) of a cache [n_pages, heads, page, D]."""
+    fmt = None if k_cache is None or k_cache.dim() != 4 else _cache_types.get(k_cache.dtype)
     if fmt is None:
-        raise ValueError(f"k_cache: dtype {k_cache.dtype}, expected int8 (Q8_0), float16 or bfloat16")
-    _need(v_cache, k_cache.dtype, k_cache.shape, "v_cache")
-    n_pages, heads, page, D = k_cache.shape
-    for t, name in ((k_d, "k_d"), (v_d, "v_d")):
-        if fmt != NVQ_KV_Q8_0:
-            if t is not None:
-                raise ValueError(f"{name}: a 16-bit cache has no scales")
-        elif t is None or tuple(t.shape) != (n_pages, heads, page, D // 32) or t.element_size() != 2:
-            raise ValueError(f"{name} must be a 2-byte tensor [n_pages, heads, page, D/32]")
-    return fmt, n_pages, heads, page, D
+        raise ValueError("k_cache: an int8 (Q8_0), float16 or bfloat16 tensor [n_pages, heads, page, D] is required")
+    shape = k_cache.shape
+    p = [_dense(k_cache, k_cache.dtype, shape, "k_cache"), _dense(v_cache, k_cache.dtype, shape, "v_cache"), None, None]
+    if fmt != NVQ_KV_Q8_0:
+        if k_d is not None or v_d is not None:
+            raise ValueError("k_d, v_d: a 16-bit cache has no scales")
+        return fmt, shape, p
+    d_shape = (shape[0], shape[1], shape[2], shape[3] // 32)
+    for i, t in ((2, k_d), (3, v_d)):
+        if t is None or t.shape != d_shape or t.element_size() != 2 or not t.is_contiguous():
+            raise ValueError("k_d and v_d must be contiguous 2-byte tensors [n_pages, heads, page, D/32]")
+        p[i] = t.data_ptr()
+    return fmt, shape, p
 
 
 def _kv_copy(name, k, v, slots, k_cache, v_cache, k_d, v_d, stream):
     import torch
 
-    fmt, n_pages, heads, page, D = _kv_cache(k_cache, v_cache, k_d, v_d)
-    code = _row_type(k, "k")
-    T = k.shape[0]
-    _need(k, k.dtype, (T, heads, D), "k")
-    _need(v, k.dtype, (T, heads, D), "v")
-    _row_type(v, "v")
-    _need(slots, torch.int64, (T,), "slots")
-    _same_device(k, v, slots, k_cache, v_cache, k_d, v_d)
-    _check(getattr(lib(), name)(fmt, code, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
-                                _ptr(slots), T, heads, D, _ptr(k_cache), _ptr(v_cache), _ptr(k_d), _ptr(v_d), n_pages,
-                                page, _stream(stream, k_cache)), name)
+    L = _attn_lib()
+    fmt, (n_pages, heads, page, D), p = _kv_cache(k_cache, v_cache, k_d, v_d)
+    shape = (_row_shape(k, "k")[0], heads, D)
+    ks, vs = _rows(k, k.dtype, shape, "k"), _rows(v, k.dtype, shape, "v")
+    sp = _dense(slots, torch.int64, shape[:1], "slots")
+    on = _on_device(stream, k, v, slots, k_cache, v_cache, k_d, v_d)
+    st = getattr(L, name)(fmt, _row_types[k.dtype], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], sp, shape[0], heads, D,
+                          p[0], p[1], p[2], p[3], n_pages, page, on)
+    if st:
+        _check(st, name)
 
 
 def nvq_kv_write(k, v, slots, k_cache, v_cache, k_d=None, v_d=None, stream=None) -> None:
@@ -705,24 +730,24 @@ def nvq_attn_decode(q, k_cache, v_cache, table, lengths, out, k_d=None, v_d=None
     lengths int32 [B] -> out [B, Hq, D] of q's type.  scale: 1 / sqrt(D) unless given."""
     import torch
 
-    fmt, n_pages, heads, page, D = _kv_cache(k_cache, v_cache, k_d, v_d)
-    code = _row_type(q, "q")
-    B, Hq = q.shape[:2]
-    _need(q, q.dtype, (B, Hq, D), "q")
-    _need(out, q.dtype, (B, Hq, D), "out")
+    L = _attn_lib()
+    fmt, (n_pages, heads, page, D), p = _kv_cache(k_cache, v_cache, k_d, v_d)
+    B, Hq, _ = _row_shape(q, "q")
+    qs = _rows(q, q.dtype, (B, Hq, D), "q")
+    op = _dense(out, q.dtype, (B, Hq, D), "out")
     if table is None or table.dim() != 2:
         raise ValueError("table: int32 [B, max_pages] is required")
     max_pages = table.shape[1]
-    _need(table, torch.int32, (B, max_pages), "table")
-    _need(lengths, torch.int32, (B,), "lengths")
-    _same_device(q, k_cache, v_cache, table, lengths, out, k_d, v_d, workspace)
+    tp = _dense(table, torch.int32, (B, max_pages), "table")
+    lp = _dense(lengths, torch.int32, (B,), "lengths")
+    on = _on_device(stream, q, k_cache, v_cache, table, lengths, out, k_d, v_d, workspace)
     if workspace is None:
-        workspace = _workspace(nvq_attn_decode_workspace_bytes(B, Hq, heads, D, max_pages, page), stream, q)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().nvq_attn_decode(fmt, code, q.data_ptr(), q.stride(0), q.stride(1), B, Hq, heads, D, _ptr(k_cache),
-                                 _ptr(v_cache), _ptr(k_d), _ptr(v_d), n_pages, page, _ptr(table), max_pages,
-                                 _ptr(lengths), D ** -0.5 if scale is None else float(scale), _ptr(out),
-                                 _ptr(workspace), ws_bytes, _stream(stream, q)), "nvq_attn_decode")
+        workspace = _workspace(L.nvq_attn_decode_workspace_bytes(B, Hq, heads, D, max_pages, page), stream, q)
+    wp, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
+    st = L.nvq_attn_decode(fmt, _row_types[q.dtype], q.data_ptr(), qs[0], qs[1], B, Hq, heads, D, p[0], p[1], p[2], p[3], n_pages, page, tp,
+                           max_pages, lp, D ** -0.5 if scale is None else scale, op, wp, ws_bytes, on)
+    if st:
+        _check(st, "nvq_attn_decode")
 
 
 def _workspace(nbytes, stream, like):
@@ -744,22 +769,24 @@ def nvq_attn_prompt(q, k, v, cu_q, cu_k, out, scale=None, causal=True, stream=No
     scale: 1 / sqrt(D) unless given."""
     import torch
 
-    code = _row_type(q, "q")
-    Tq, Hq, D = q.shape
-    Tk, Hkv = k.shape[:2] if k is not None and k.dim() == 3 else (-1, -1)
-    for t, name, shape in ((k, "k", (Tk, Hkv, D)), (v, "v", (Tk, Hkv, D)), (out, "out", (Tq, Hq, D))):
-        _need(t, q.dtype, shape, name)
-        _row_type(t, name)
-    B = cu_q.shape[0] - 1 if cu_q is not None and cu_q.dim() == 1 else -1
-    if B < 0:
+    L = _attn_lib()
+    Tq, Hq, D = _row_shape(q, "q")
+    Tk, Hkv, _ = _row_shape(k, "k")
+    t = q.dtype
+    qs, ks, vs = _rows(q, t, (Tq, Hq, D), "q"), _rows(k, t, (Tk, Hkv, D), "k"), _rows(v, t, (Tk, Hkv, D), "v")
+    os_ = _rows(out, t, (Tq, Hq, D), "out")
+    if cu_q is None or cu_q.dim() != 1 or cu_q.shape[0] < 1:
         raise ValueError("cu_q: int32 [B + 1] is required")
-    _need(cu_q, torch.int32, (B + 1,), "cu_q")
-    _need(cu_k, torch.int32, (B + 1,), "cu_k")
-    _same_device(q, k, v, cu_q, cu_k, out)
-    strides = (ctypes.c_int64 * 8)(*(s for t in (q, k, v, out) for s in t.stride()[:2]))
-    _check(lib().nvq_attn_prompt(code, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), strides, _ptr(cu_q),
-                                 _ptr(cu_k), B, Tq, Tk, Hq, Hkv, D, D ** -0.5 if scale is None else float(scale),
-                                 1 if causal else 0, _stream(stream, q)), "nvq_attn_prompt")
+    cq, ck = _dense(cu_q, torch.int32, cu_q.shape, "cu_q"), _dense(cu_k, torch.int32, cu_q.shape, "cu_k")
+    on = _on_device(stream, q, k, v, cu_q, cu_k, out)
+    strides = _Strides(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
+    st = L.nvq_attn_prompt(_row_types[t], q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), strides, cq, ck, cu_q.shape[0] - 1, Tq, Tk,
+                           Hq, Hkv, D, D ** -0.5 if scale is None else scale, 1 if causal else 0, on)
+    if st:
+        _check(st, "nvq_attn_prompt")
+
+
+_Strides = ctypes.c_int64 * 8
 
 
 # ---------------------------------------------------------------------------

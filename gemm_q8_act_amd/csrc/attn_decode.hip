@@ -27,10 +27,10 @@ namespace nvq {
 
 namespace {
 
-constexpr int kWaves = 4;
 constexpr int kTile = 32;          // keys of one wavefront's step
-constexpr int kMinChunk = 256;     // keys
-constexpr int kTargetGroups = 1024;
+constexpr int kMinChunk = 128;     // keys
+constexpr int kTargetGroups = 512;
+constexpr int kJoinWaves = 8;
 // A score may pass the running maximum by 2^kSlack before everything is rescaled.
 constexpr float kSlack = 8.0f;
 // Over a binary16 cache P (at most 2^kSlack) goes in times this: both its terms stay inside
@@ -78,12 +78,14 @@ __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int want, bool wa
     const int n = a.lengths[i];
     total += n < 0 || n > cap ? 0 : n;
   }
-  total = wave_sum(total);
+  total = __builtin_amdgcn_readfirstlane(wave_sum(total));
   Plan p;
-  // chunk >= total / target, so there are at most target + B chunks; a multiple of a step
-  // of all four wavefronts
-  const uint32_t unit = kTile * kWaves;
-  const uint32_t even = ((uint32_t)total + (uint32_t)a.target - 1) / (uint32_t)a.target;
+  // chunk >= total / target, so there are at most target + B chunks (chunk_bound); a multiple of
+  // a step of four wavefronts
+  const uint32_t unit = kTile * 4;
+  // (every sequence's last chunk is a part of one: half of one is taken off for each)
+  const uint32_t whole = (uint32_t)max(a.target - a.B / 2, (a.target + 3) / 4);
+  const uint32_t even = ((uint32_t)total + whole - 1) / whole;
   p.chunk = max(kMinChunk, (int)((even + unit - 1) / unit * unit));
   int base = 0;
   p.b = -1;
@@ -114,10 +116,10 @@ __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int want, bool wa
   return p;
 }
 
-// N dwords from an address that is a multiple of 4 N bytes (up to 16) away from a 16-byte
-// aligned one
+// N dwords of LDS from an address that is a multiple of 4 N bytes (up to 16) away from a
+// 16-byte aligned one
 template <int N>
-__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t* v) {
+__device__ __forceinline__ void read_dwords(const uint8_t* p, uint32_t* v) {
   if constexpr (N % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
@@ -149,49 +151,48 @@ struct Shape {
   typedef typename CacheType<Q8 ? NVQ_KV_BF16 : FMT>::type P;
   static constexpr int P_TERMS = Q8 || FMT == NVQ_KV_BF16 ? 3 : 2;
   static constexpr int TILES = 2 * NB;                // 16-channel tiles of the result
+  // LDS of a tile: two 16-key groups of keys, the same of values, then both groups' key
+  // scales and value scales
+  static constexpr int GROUP = 16 * ROW, SCALES = Q8 ? 32 * NB : 0;
+  static constexpr int SLOT = 4 * GROUP + 4 * SCALES;
+  // Two tiles' room a wavefront.  Rows wider than 256 bytes leave room for two wavefronts.
+  static constexpr int WAVES = 2 * 4 * SLOT <= 144 * 1024 ? 4 : 2;
+  // 16-byte pieces of a key row, and which row bits they are exchanged by in LDS, so that the
+  // lanes of one piece of different rows fall on different banks (64 of 4 bytes)
+  static constexpr int PIECES = ROW / 16;
+  static constexpr bool SWIZZLE = (PIECES & (PIECES - 1)) == 0 && PIECES >= 4;
+  static constexpr int SWIZZLE_SHIFT = PIECES >= 16 ? 0 : PIECES == 8 ? 1 : 2;
+  // load instructions (1 KB each, or what is left) of a group; of a tile's keys with all scales
+  static constexpr int LOADS = (GROUP + 1023) / 1024;
+  static constexpr int K_LOADS = 2 * LOADS + (Q8 ? 1 : 0), V_LOADS = 2 * LOADS;
+  static __device__ __forceinline__ int piece(int row, int i) { return SWIZZLE ? i ^ ((row >> SWIZZLE_SHIFT) & (PIECES - 1)) : i; }
 };
 
-// One wavefront's 32 keys: group u holds keys base_u .. base_u + 15, all in one page.
-template <int FMT, int NB>
-struct Tile {
-  typedef Shape<FMT, NB> S;
-  uint32_t k[2][S::KW];
-  uint32_t v[2][4][S::VW];
-  uint32_t kd[2][S::DW], vd[2][S::DW];
-};
-
-template <int FMT, int NB>
-__device__ __forceinline__ void load_group(const DecodeArgs& a, int64_t row0, int u, Tile<FMT, NB>& t) {
-  typedef Shape<FMT, NB> S;
-  const int lane = (int)(threadIdx.x & 63), n = lane & 15, g = lane >> 4;
-  const uint8_t* k = reinterpret_cast<const uint8_t*>(a.c.k) + row0 * S::ROW;
-  const uint8_t* v = reinterpret_cast<const uint8_t*>(a.c.v) + row0 * S::ROW;
-  if constexpr (S::Q8) {
-    load_dwords<S::KW>(k + (uint32_t)(n * S::ROW + 8 * NB * g), t.k[u]);
-  } else {
-#pragma unroll
-    for (int b = 0; b < NB; ++b) load_dwords<4>(k + (uint32_t)(n * S::ROW + 64 * b + 16 * g), t.k[u] + 4 * b);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (S::Q8) {
-      const uint8_t* p = v + (uint32_t)((4 * g + i) * S::ROW + 2 * NB * n);
-      if constexpr (NB % 2 == 0) {
-        load_dwords<S::VW>(p, t.v[u][i]);
-      } else {
-        const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-        for (int b = 0; b < NB; b += 2) t.v[u][i][b / 2] = h[b] | (b + 1 < NB ? (uint32_t)h[b + 1] << 16 : 0u);
-      }
-    } else {
-      load_dwords<S::VW>(v + (uint32_t)((4 * g + i) * S::ROW + 4 * NB * n), t.v[u][i]);
-    }
-  }
-  if constexpr (S::Q8) {
-    load_dwords<S::DW>(reinterpret_cast<const uint8_t*>(a.c.k_d) + row0 * (2 * NB) + (uint32_t)(8 * NB * g), t.kd[u]);
-    load_dwords<S::DW>(reinterpret_cast<const uint8_t*>(a.c.v_d) + row0 * (2 * NB) + (uint32_t)(8 * NB * g), t.vd[u]);
-  }
+// 16 bytes a lane from base + offset straight into LDS, lane after lane from `lds` on.  In
+// assembly because the compiler, which cannot tell one part of LDS from another, waits for
+// every such load before any LDS read; here the waits are written out (wait_loads).
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(offset), "s"(base), "s"(lds) : "memory", "m0");
 }
+// The same with an address a lane.
+__device__ __forceinline__ void load_to_lds_far(const uint8_t* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(p), "s"(lds) : "memory", "m0");
+}
+// Where the lane's 16 bytes of load i of a group of key rows come from: LDS takes the pieces in
+// order, so the exchange is made on this side.
+template <int FMT, int NB>
+__device__ __forceinline__ uint32_t swizzled_offset(int lane, int i) {
+  typedef Shape<FMT, NB> S;
+  const int at = 64 * i + lane, row = at / S::PIECES;
+  return (uint32_t)(row * S::ROW + 16 * S::piece(row, at % S::PIECES));
+}
+// Until at most N of the wavefront's loads are on their way (they come back in order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Until the LDS reads so far have their data: what they read may be loaded over.
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ float half_of(const uint32_t* w, int i) {
   return f16_bits_to_f32((uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]));
@@ -225,9 +226,67 @@ __device__ __forceinline__ void split_terms(const float (&x)[8], Frag (&f)[TERMS
   }
 }
 
+// The lane's 8 channels of each 32-block of a query row, from element `at` on.
+template <int NB>
+__device__ __forceinline__ void load_queries(const DecodeArgs& a, int64_t at, u32x4 (&raw)[NB][2]) {
+  if (a.type == NVQ_TYPE_F32) {
+    const float* p = reinterpret_cast<const float*>(a.q) + at;
+#pragma unroll
+    for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) raw[bl][i] = *reinterpret_cast<const u32x4*>(p + 32 * bl + 4 * i);
+  } else {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) + at;
+#pragma unroll
+    for (int bl = 0; bl < NB; ++bl) raw[bl][0] = *reinterpret_cast<const u32x4*>(p + 32 * bl), raw[bl][1] = u32x4{0, 0, 0, 0};
+  }
+}
+
+// Their operands; over binary16 operands scaled to 2^7 .. 2^8 by a power of two, whose inverse is
+// returned.
 template <int FMT, int NB>
-__global__ __launch_bounds__(64 * kWaves, NB <= 3 ? 2 : 1) void attn_decode_kernel(DecodeArgs a) {
+__device__ __forceinline__ float split_queries(int type, const u32x4 (&raw)[NB][2], Frag (&qf)[NB][Shape<FMT, NB>::TERMS]) {
   typedef Shape<FMT, NB> S;
+  float x[NB][8];
+#pragma unroll
+  for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float t[2];
+      if (type == NVQ_TYPE_F32) {
+        const uint32_t u = raw[bl][i >> 1][2 * (i & 1)], v = raw[bl][i >> 1][2 * (i & 1) + 1];
+        t[0] = __builtin_bit_cast(float, u), t[1] = __builtin_bit_cast(float, v);
+      } else if (type == NVQ_TYPE_F16) {
+        unpack_pair<_Float16>(raw[bl][0][i], t);
+      } else {
+        unpack_pair<__bf16>(raw[bl][0][i], t);
+      }
+      x[bl][2 * i] = t[0], x[bl][2 * i + 1] = t[1];
+    }
+  float back = 1.0f;
+  if constexpr (FMT != NVQ_KV_BF16) {
+    float top = 0.0f;
+#pragma unroll
+    for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[bl][i]));
+    top = max_32(max_16(top));
+    const int e = top > 0.0f && top < __builtin_inff() ? 8 - __builtin_amdgcn_frexp_expf(top) : 0;
+#pragma unroll
+    for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[bl][i] = __builtin_amdgcn_ldexpf(x[bl][i], e);
+    back = __builtin_amdgcn_ldexpf(1.0f, -e);
+  }
+#pragma unroll
+  for (int bl = 0; bl < NB; ++bl) split_terms<typename CacheType<FMT>::type, S::TERMS>(x[bl], qf[bl]);
+  return back;
+}
+
+template <int FMT, int NB>
+__global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES)) void attn_decode_kernel(DecodeArgs a) {
+  typedef Shape<FMT, NB> S;
+  constexpr int kWaves = S::WAVES;
   typedef typename CacheType<FMT>::type T;
   const int lane = (int)(threadIdx.x & 63), n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -239,35 +298,11 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 3 ? 2 : 1) void attn_decode_kern
   const int b = plan.b;
   const int k0 = (c - plan.first) * plan.chunk, k1 = min(plan.len, k0 + plan.chunk);
 
-  // The query heads' rows, scaled to 2^7 .. 2^8 by a power of two (binary16 terms), in the
-  // keys' operand order: block bl, slot (g, s) is channel 32 bl + 8 g + s.
+  // The query heads' rows on their way, in the keys' operand order: block bl, slot (g, s) is
+  // channel 32 bl + 8 g + s.  Columns past the last head read it again.
   const bool live = h0 + n < a.G;
-  Frag qf[NB][S::TERMS];
-  float to_log2 = a.scale_log2;
-  {
-    float x[NB][8];
-    float top = 0.0f;
-#pragma unroll
-    for (int bl = 0; bl < NB; ++bl) {
-      if (live)
-        load_8(a.q, a.type, b * a.q_stride_b + (int64_t)(kvh * a.G + h0 + n) * a.q_stride_h + 32 * bl + 8 * g, x[bl]);
-      else
-        for (int i = 0; i < 8; ++i) x[bl][i] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[bl][i]));
-    }
-    if constexpr (FMT != NVQ_KV_BF16) {
-      top = max_32(max_16(top));
-      const int e = top > 0.0f && top < __builtin_inff() ? 8 - __builtin_amdgcn_frexp_expf(top) : 0;
-#pragma unroll
-      for (int bl = 0; bl < NB; ++bl)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[bl][i] = __builtin_amdgcn_ldexpf(x[bl][i], e);
-      to_log2 = __builtin_amdgcn_ldexpf(to_log2, -e);
-    }
-#pragma unroll
-    for (int bl = 0; bl < NB; ++bl) split_terms<T, S::TERMS>(x[bl], qf[bl]);
-  }
+  u32x4 q_raw[NB][2];
+  load_queries<NB>(a, b * a.q_stride_b + (int64_t)(kvh * a.G + min(h0 + n, a.G - 1)) * a.q_stride_h + 8 * g, q_raw);
 
   floatx4 acc[S::TILES];
 #pragma unroll
@@ -275,24 +310,105 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 3 ? 2 : 1) void attn_decode_kern
   float m = -__builtin_inff(), l = 0.0f;
   bool bad_page = false;
 
-  const int32_t* table = a.table + (int64_t)b * a.table_stride;
+  // The wavefront's tiles are s0, s0 + kWaves, ..; tile number t of them sits in slot t % 2.
+  constexpr int kJoin = (kWaves - 1) * S::TILES * 64 * 16;
+  __shared__ __align__(16) uint8_t s_ring[kWaves * 2 * S::SLOT > kJoin ? kWaves * 2 * S::SLOT : kJoin];
+  uint8_t* const ring = s_ring + wave * (2 * S::SLOT);
+  const uint32_t ring_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)ring);
+  const auto* table = (const __attribute__((address_space(4))) int32_t*)(a.table + (int64_t)b * a.table_stride);
   const int steps = (k1 - k0 + kTile - 1) / kTile;
+  const int mine = steps > wave ? (steps - wave + kWaves - 1) / kWaves : 0;
   const int page_mask = (1 << a.c.page_shift) - 1;
-  const auto load_tile = [&](int s, Tile<FMT, NB>& t) {
+  // a group past the end is the last group again (its scores are masked)
+  const auto key_of = [&](int t, int u) __attribute__((always_inline)) { return min(k0 + (wave + t * kWaves) * kTile + 16 * u, (k1 - 1) & ~15); };
+  const auto page_of = [&](int t, int u) __attribute__((always_inline)) { return mine > 0 ? table[key_of(t, u) >> a.c.page_shift] : 0; };
+  // the cache rows of both groups of the tile that is loaded next (plain variables: an array
+  // here would be kept in memory)
+  int page_a = 0, page_b = 0;
+  int64_t row_a = 0, row_b = 0;
+  const auto row_in = [&](int page, int key) __attribute__((always_inline)) {
+    const bool out = (uint32_t)page >= (uint32_t)a.c.n_pages;
+    bad_page |= out;
+    return (((int64_t)(out ? 0 : page) * a.Hkv + kvh) << a.c.page_shift) + (key & page_mask);
+  };
+  const auto look_up = [&](int t) __attribute__((always_inline)) { page_a = page_of(t, 0), page_b = page_of(t, 1); };
+  const auto find_rows = [&](int t) __attribute__((always_inline)) { row_a = row_in(page_a, key_of(t, 0)), row_b = row_in(page_b, key_of(t, 1)); };
+  const auto load_rows = [&](const void* codes, uint32_t at, bool keys) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      // a group past the end reads the last group again (its scores are masked)
-      const int key = min(k0 + s * kTile + 16 * u, (k1 - 1) & ~15);
-      int pg = table[key >> a.c.page_shift];
-      const bool out = (uint32_t)pg >= (uint32_t)a.c.n_pages;
-      bad_page |= out;
-      pg = out ? 0 : pg;
-      load_group<FMT, NB>(a, (((int64_t)pg * a.Hkv + kvh) << a.c.page_shift) + (key & page_mask), u, t);
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < S::LOADS; ++i) {
+        const uint32_t offset = S::SWIZZLE && keys ? swizzled_offset<FMT, NB>(lane, i) : (uint32_t)(16 * lane + 1024 * i);
+        if (1024 * (i + 1) <= S::GROUP || 16 * lane + 1024 * i < S::GROUP)
+          load_to_lds(reinterpret_cast<const uint8_t*>(codes) + (u ? row_b : row_a) * S::ROW, offset, at + u * S::GROUP + 1024 * i);
+      }
+  };
+  const auto load_keys = [&](uint32_t at) __attribute__((always_inline)) {
+    load_rows(a.c.k, at, true);
+    if constexpr (S::Q8) {
+      // lanes: 2 NB pieces each of the key scales of group 0, group 1, the value scales' 0, 1
+      const int which = lane / (2 * NB), i = lane % (2 * NB);
+      const uint8_t* kd = reinterpret_cast<const uint8_t*>(a.c.k_d);
+      const int64_t row = (which & 1) ? row_b : row_a;
+      const uint8_t* p = (which & 2 ? reinterpret_cast<const uint8_t*>(a.c.v_d) : kd) + row * (2 * NB) + 16 * i;
+      if (lane < 8 * NB) load_to_lds_far(p, at + 4 * S::GROUP);
     }
   };
+  const auto load_values = [&](uint32_t at) __attribute__((always_inline)) { load_rows(a.c.v, at + 2 * S::GROUP, false); };
 
-  const auto step = [&](int s, Tile<FMT, NB>& t) {
-    const int key0 = k0 + s * kTile;
+  if (mine > 0) {
+    look_up(0);
+    find_rows(0);
+    load_keys(ring_at);
+    load_values(ring_at);
+    if (mine > 1) look_up(1);
+  }
+  // (the first use of the queries waits for all loads so far: the first tile is among them,
+  // the second one follows)
+  Frag qf[NB][S::TERMS];
+  const float to_log2 = a.scale_log2 * split_queries<FMT, NB>(a.type, q_raw, qf);
+  if (mine > 1) {
+    find_rows(1);
+    load_keys(ring_at + S::SLOT);
+    load_values(ring_at + S::SLOT);
+    if (mine > 2) look_up(2);
+  }
+
+  for (int t = 0; t < mine; ++t) {
+    const int key0 = k0 + (wave + t * kWaves) * kTile;
+    const uint8_t* slot = ring + (t & 1) * S::SLOT;
+    const uint32_t slot_at = ring_at + (t & 1) * S::SLOT;
+    // outstanding behind this tile's keys: its values and the next tile
+    if (t + 1 < mine)
+      wait_loads<S::V_LOADS + S::K_LOADS + S::V_LOADS>();
+    else
+      wait_loads<S::V_LOADS>();
+    uint32_t kw[2][S::KW], kd[2][S::DW], vd[2][S::DW];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* p = slot + u * S::GROUP + n * S::ROW;
+      if constexpr (S::Q8 && S::SWIZZLE) {
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) read_dwords<4>(p + 16 * S::piece(n, NB / 2 * g + i), kw[u] + 4 * i);
+      } else if constexpr (S::Q8) {
+        read_dwords<S::KW>(p + 8 * NB * g, kw[u]);
+      } else {
+#pragma unroll
+        for (int bl = 0; bl < NB; ++bl) read_dwords<4>(p + 16 * S::piece(n, 4 * bl + g), kw[u] + 4 * bl);
+      }
+      if constexpr (S::Q8) {
+        const uint8_t* d = slot + 4 * S::GROUP + u * S::SCALES + 8 * NB * g;
+        read_dwords<S::DW>(d, kd[u]);
+        read_dwords<S::DW>(d + 2 * S::SCALES, vd[u]);
+      }
+    }
+    const bool more = t + 2 < mine;
+    if (more) {
+      find_rows(t + 2);
+      wait_reads();
+      load_keys(slot_at);
+      if (t + 3 < mine) look_up(t + 3);
+    }
     float sc[8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -304,17 +420,17 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 3 ? 2 : 1) void attn_decode_kern
 #pragma unroll
           for (int j = 0; j < 4; ++j) {  // the pair of channels 32 bl + 8 g + 2 j, + 1
             const int at = 2 * NB * j + 2 * bl;
-            const uint32_t w = perm(0x64646464u, t.k[u][at / 4] ^ 0x80808080u, at & 2 ? 0x04030402u : 0x04010400u);
+            const uint32_t w = perm(0x64646464u, kw[u][at / 4] ^ 0x80808080u, at & 2 ? 0x04030402u : 0x04010400u);
             f.v[j] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, w) - half2_t{(_Float16)1152.0f, (_Float16)1152.0f});
           }
           floatx4 part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int e = 0; e < S::TERMS; ++e) part = mfma16<T>(f, qf[bl][e], part);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum[i] = __builtin_fmaf(half_of(t.kd[u], i * NB + bl), part[i], sum[i]);
+          for (int i = 0; i < 4; ++i) sum[i] = __builtin_fmaf(half_of(kd[u], i * NB + bl), part[i], sum[i]);
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) f.v[j] = t.k[u][4 * bl + j];
+          for (int j = 0; j < 4; ++j) f.v[j] = kw[u][4 * bl + j];
 #pragma unroll
           for (int e = 0; e < S::TERMS; ++e) sum = mfma16<T>(f, qf[bl][e], sum);
         }
@@ -322,6 +438,34 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 3 ? 2 : 1) void attn_decode_kern
 #pragma unroll
       for (int i = 0; i < 4; ++i) sc[4 * u + i] = sum[i] * to_log2;
     }
+
+    if (more)
+      wait_loads<S::K_LOADS + S::V_LOADS + S::K_LOADS>();
+    else if (t + 1 < mine)
+      wait_loads<S::K_LOADS + S::V_LOADS>();
+    else
+      wait_loads<0>();
+    uint32_t vw[2][4][S::VW];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* p = slot + (2 + u) * S::GROUP + (4 * g + i) * S::ROW;
+        if constexpr (!S::Q8) {
+          read_dwords<S::VW>(p + 4 * NB * n, vw[u][i]);
+        } else if constexpr (NB % 2 == 0) {
+          read_dwords<S::VW>(p + 2 * NB * n, vw[u][i]);
+        } else {
+          const uint16_t* h = reinterpret_cast<const uint16_t*>(p + 2 * NB * n);
+#pragma unroll
+          for (int bl = 0; bl < NB; bl += 2) vw[u][i][bl / 2] = h[bl] | (bl + 1 < NB ? (uint32_t)h[bl + 1] << 16 : 0u);
+        }
+      }
+    if (more) {
+      wait_reads();
+      load_values(slot_at);
+    }
+
     if (key0 + kTile > k1) {
       // keys past the end: no probability, and nothing of what their rows hold (never written,
       // perhaps NaN) may reach the products
@@ -335,11 +479,11 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 3 ? 2 : 1) void attn_decode_kern
 #pragma unroll
               for (int bl = 0; bl < NB; ++bl) {
                 const int at = i * NB + bl;
-                t.vd[u][at >> 1] &= at & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                vd[u][at >> 1] &= at & 1 ? 0x0000FFFFu : 0xFFFF0000u;
               }
             } else {
 #pragma unroll
-              for (int w = 0; w < S::VW; ++w) t.v[u][i][w] = 0;
+              for (int w = 0; w < S::VW; ++w) vw[u][i][w] = 0;
             }
           }
     }
@@ -370,7 +514,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 3 ? 2 : 1) void attn_decode_kern
       for (int bl = 0; bl < NB; ++bl) {
         float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = p[i] * half_of(t.vd[i >> 2], (i & 3) * NB + bl);
+        for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(half_of(vd[i >> 2], (i & 3) * NB + bl), p[i], 0.0f);
         Frag pf[S::P_TERMS];
         split_terms<typename S::P, S::P_TERMS>(x, pf);
 #pragma unroll
@@ -379,7 +523,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 3 ? 2 : 1) void attn_decode_kern
           const int at = 2 * bl + e;
 #pragma unroll
           for (int j = 0; j < 4; ++j)  // keys 2 j, 2 j + 1 of the lane's eight
-            f.v[j] = codes_to_bf16(t.v[j >> 1][2 * (j & 1)][at >> 2], t.v[j >> 1][2 * (j & 1) + 1][at >> 2], at & 3);
+            f.v[j] = codes_to_bf16(vw[j >> 1][2 * (j & 1)][at >> 2], vw[j >> 1][2 * (j & 1) + 1][at >> 2], at & 3);
 #pragma unroll
           for (int k = 0; k < S::P_TERMS; ++k) acc[2 * bl + e] = mfma16<typename S::P>(f, pf[k], acc[2 * bl + e]);
         }
@@ -392,33 +536,16 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 3 ? 2 : 1) void attn_decode_kern
         Frag f;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          f.v[j] = perm(t.v[j >> 1][2 * (j & 1) + 1][i >> 1], t.v[j >> 1][2 * (j & 1)][i >> 1], i & 1 ? 0x07060302u : 0x05040100u);
+          f.v[j] = perm(vw[j >> 1][2 * (j & 1) + 1][i >> 1], vw[j >> 1][2 * (j & 1)][i >> 1], i & 1 ? 0x07060302u : 0x05040100u);
 #pragma unroll
         for (int k = 0; k < S::P_TERMS; ++k) acc[i] = mfma16<typename S::P>(f, pf[k], acc[i]);
       }
-    }
-  };
-
-  // one tile in flight while the one before is computed
-  Tile<FMT, NB> ta, tb;
-  int s = wave;
-  if (s < steps) {
-    load_tile(s, ta);
-    while (true) {
-      if (s + kWaves < steps) load_tile(s + kWaves, tb);
-      step(s, ta);
-      s += kWaves;
-      if (s >= steps) break;
-      if (s + kWaves < steps) load_tile(s + kWaves, ta);
-      step(s, tb);
-      s += kWaves;
-      if (s >= steps) break;
     }
   }
 
   // Join the wavefronts.
   __shared__ float s_m[kWaves][16], s_l[kWaves][16];
-  __shared__ floatx4 s_acc[kWaves - 1][S::TILES][64];
+  floatx4* const s_acc = reinterpret_cast<floatx4*>(s_ring);  // [kWaves - 1][TILES][64]; the tiles have been read
   l = sum_32(sum_16(l));
   if (bad_page || plan.bad) l = __builtin_nanf("");
   if (g == 0) s_m[wave][n] = m, s_l[wave][n] = l;
@@ -432,7 +559,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 3 ? 2 : 1) void attn_decode_kern
   for (int t = 0; t < S::TILES; ++t) acc[t] *= wt;
   if (wave != 0) {
 #pragma unroll
-    for (int t = 0; t < S::TILES; ++t) s_acc[wave - 1][t][lane] = acc[t];
+    for (int t = 0; t < S::TILES; ++t) s_acc[((wave - 1) * S::TILES + t) * 64 + lane] = acc[t];
   }
   __syncthreads();
   if (wave != 0) return;
@@ -442,7 +569,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 3 ? 2 : 1) void attn_decode_kern
 #pragma unroll
   for (int w = 0; w < kWaves - 1; ++w)
 #pragma unroll
-    for (int t = 0; t < S::TILES; ++t) acc[t] += s_acc[w][t][lane];
+    for (int t = 0; t < S::TILES; ++t) acc[t] += s_acc[(w * S::TILES + t) * 64 + lane];
 
   if (plan.count > 1) {
     floatx4* dst = reinterpret_cast<floatx4*>(a.acc) + (int64_t)blockIdx.x * (S::TILES * 64) + lane;
@@ -477,40 +604,72 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 3 ? 2 : 1) void attn_decode_kern
   }
 }
 
-// Joins the chunks of sequence blockIdx.x / (Hkv HT) in their order: blockIdx.y is one
-// 16-channel tile, a wavefront takes every fourth chunk.
-template <int FMT, int NB>
-__global__ __launch_bounds__(64 * kWaves) void attn_decode_join_kernel(DecodeArgs a) {
+// Joins the chunks of sequence blockIdx.x / (Hkv HT) in their order.  Of a workgroup's eight
+// wavefronts, APART take 16-channel tiles of their own and the others share those tiles'
+// chunks: all eight apart where there are sequences enough to fill the chip (64 sequences of
+// about 4 chunks, 128 channels: 5 us; sharing 15), none where a few sequences have many chunks.
+template <int FMT, int NB, int APART>
+__global__ __launch_bounds__(64 * kJoinWaves) void attn_decode_join_kernel(DecodeArgs a) {
   typedef Shape<FMT, NB> S;
+  constexpr int kWaves = kJoinWaves / APART;
   const int lane = (int)(threadIdx.x & 63), n = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wave_id = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int own_tile = wave_id % APART, wave = wave_id / APART;
   const int per = a.Hkv * a.HT;
-  const int b = (int)blockIdx.x / per, hh = (int)blockIdx.x - b * per, tile = (int)blockIdx.y;
+  const int b = (int)blockIdx.x / per, hh = (int)blockIdx.x - b * per;
+  const bool in = (int)blockIdx.y * APART + own_tile < S::TILES;
+  const int tile = min((int)blockIdx.y * APART + own_tile, S::TILES - 1);
   const Plan plan = make_plan(a, b, true);
   if (plan.count <= 1) return;
+  // per is the distance of a sequence's chunks; a wavefront takes chunks wave, wave + kWaves, ..,
+  // four at a time with all their loads in flight, with a running maximum of its own
   const float* stat = a.stat + ((int64_t)plan.first * per + hh) * 32 + n;
-  const int64_t stat_step = (int64_t)per * 32;
-  float all = -__builtin_inff();
-  for (int c = g; c < plan.count; c += 4) all = fmaxf(all, stat[c * stat_step]);
-  all = max_32(max_16(all));
   const floatx4* src = reinterpret_cast<const floatx4*>(a.acc) + ((int64_t)plan.first * per + hh) * (S::TILES * 64) + tile * 64 + lane;
-  const int64_t step = (int64_t)per * (S::TILES * 64);
   floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-  float sum = 0.0f;
-#pragma unroll 8
-  for (int c = wave; c < plan.count; c += kWaves) {
-    const float m = stat[c * stat_step];
-    const float w = m == -__builtin_inff() ? 0.0f : exp2_fast(m - all);
-    acc += src[c * step] * w;
-    sum += stat[c * stat_step + 16] * w;
-  }
-  __shared__ floatx4 s_acc[kWaves - 1][64];
-  __shared__ float s_sum[kWaves - 1][64];
-  if (wave != 0) s_acc[wave - 1][lane] = acc, s_sum[wave - 1][lane] = sum;
-  __syncthreads();
-  if (wave != 0) return;
+  float sum = 0.0f, top = -__builtin_inff();
+  constexpr int kBatch = 4;
+  for (int c0 = wave; c0 < plan.count; c0 += kBatch * kWaves) {
+    floatx4 part[kBatch];
+    float m[kBatch], l[kBatch];
 #pragma unroll
-  for (int w = 0; w < kWaves - 1; ++w) acc += s_acc[w][lane], sum += s_sum[w][lane];
+    for (int j = 0; j < kBatch; ++j) {
+      const int64_t c = (int64_t)min(c0 + j * kWaves, plan.count - 1) * per;
+      part[j] = src[c * (S::TILES * 64)];
+      m[j] = stat[c * 32], l[j] = stat[c * 32 + 16];
+    }
+    float m_new = top;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (c0 + j * kWaves >= plan.count) m[j] = -__builtin_inff(), l[j] = 0.0f, part[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+      m_new = fmaxf(m_new, m[j]);
+    }
+    const float f = m_new == -__builtin_inff() ? 1.0f : exp2_fast(top - m_new);
+    acc *= f, sum *= f;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const float w = m[j] == -__builtin_inff() ? 0.0f : exp2_fast(m[j] - m_new);
+      acc += part[j] * w, sum += l[j] * w;
+    }
+    top = m_new;
+  }
+  if constexpr (kWaves > 1) {
+    __shared__ float s_top[kWaves][16], s_sum[kWaves - 1][64];
+    __shared__ floatx4 s_acc[kWaves - 1][64];
+    static_assert(APART == 1, "one tile to a workgroup whose wavefronts share it");
+    if (g == 0) s_top[wave][n] = top;
+    __syncthreads();
+    float all = s_top[0][n];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) all = fmaxf(all, s_top[w][n]);
+    const float own = top == -__builtin_inff() ? 0.0f : exp2_fast(top - all);
+    acc *= own, sum *= own;
+    if (wave != 0) s_acc[wave - 1][lane] = acc, s_sum[wave - 1][lane] = sum;
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int w = 0; w < kWaves - 1; ++w) acc += s_acc[w][lane], sum += s_sum[w][lane];
+  }
+  if (!in) return;
   const int kvh = hh / a.HT, h0 = (hh - kvh * a.HT) * 16;
   if (h0 + n >= a.G) return;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -537,10 +696,14 @@ int64_t chunk_bound(int64_t B, int64_t Hkv, int64_t G, int64_t capacity) {
 
 template <int FMT, int NB>
 hipError_t launch_nb(const DecodeArgs& a, int64_t blocks, bool join, hipStream_t s) {
-  hipLaunchKernelGGL((attn_decode_kernel<FMT, NB>), dim3((unsigned)blocks), dim3(64 * kWaves), 0, s, a);
+  hipLaunchKernelGGL((attn_decode_kernel<FMT, NB>), dim3((unsigned)blocks), dim3(64 * Shape<FMT, NB>::WAVES), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !join) return e;
-  hipLaunchKernelGGL((attn_decode_join_kernel<FMT, NB>), dim3((unsigned)(a.B * a.Hkv * a.HT), 2 * NB), dim3(64 * kWaves), 0, s, a);
+  const unsigned rows = (unsigned)(a.B * a.Hkv * a.HT);
+  if (rows >= 256)
+    hipLaunchKernelGGL((attn_decode_join_kernel<FMT, NB, kJoinWaves>), dim3(rows, (2 * NB + kJoinWaves - 1) / kJoinWaves), dim3(64 * kJoinWaves), 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_decode_join_kernel<FMT, NB, 1>), dim3(rows, 2 * NB), dim3(64 * kJoinWaves), 0, s, a);
   return hipGetLastError();
 }
 template <int FMT>

@@ -82,11 +82,11 @@ def test_nothing_to_do_is_ok():
 
 def test_decode_workspace_sizes():
     ws = nvq.nvq_attn_decode_workspace_bytes
-    assert ws(1, 40, 8, 128, 4, 64) == 0                 # at most 256 keys: one part to a sequence
+    assert ws(1, 40, 8, 128, 2, 64) == 0                 # at most 128 keys: one part to a sequence
     one = 8 * 64 * 16 + 2 * 16 * 4                       # a part: 128 channels and 2 statistics of 16 heads
-    assert ws(1, 40, 8, 128, 8, 64) == 2 * 8 * one       # 512 keys: two parts
-    assert ws(4, 40, 8, 128, 8, 64) == 4 * 2 * 8 * one
-    assert ws(1, 34, 2, 128, 8, 64) == 2 * 2 * 2 * one   # 17 heads to a key head: two tiles of heads
+    assert ws(1, 40, 8, 128, 4, 64) == 2 * 8 * one       # 256 keys: two parts
+    assert ws(4, 40, 8, 128, 4, 64) == 4 * 2 * 8 * one
+    assert ws(1, 34, 2, 128, 4, 64) == 2 * 2 * 2 * one   # 17 heads to a key head: two tiles of heads
     assert ws(1, 41, 8, 128, 8, 64) == 0 and ws(1, 40, 8, 100, 8, 64) == 0 and ws(0, 40, 8, 128, 8, 64) == 0
 
 
