@@ -168,16 +168,6 @@ struct Shape {
   static __device__ __forceinline__ int piece(int row, int i) { return SWIZZLE ? i ^ ((row >> SWIZZLE_SHIFT) & (PIECES - 1)) : i; }
 };
 
-// 16 bytes a lane from base + offset straight into LDS, lane after lane from `lds` on.  In
-// assembly because the compiler, which cannot tell one part of LDS from another, waits for
-// every such load before any LDS read; here the waits are written out (wait_loads).
-__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(offset), "s"(base), "s"(lds) : "memory", "m0");
-}
-// The same with an address a lane.
-__device__ __forceinline__ void load_to_lds_far(const uint8_t* p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(p), "s"(lds) : "memory", "m0");
-}
 // Where the lane's 16 bytes of load i of a group of key rows come from: LDS takes the pieces in
 // order, so the exchange is made on this side.
 template <int FMT, int NB>
@@ -186,14 +176,6 @@ __device__ __forceinline__ uint32_t swizzled_offset(int lane, int i) {
   const int at = 64 * i + lane, row = at / S::PIECES;
   return (uint32_t)(row * S::ROW + 16 * S::piece(row, at % S::PIECES));
 }
-// Until at most N of the wavefront's loads are on their way (they come back in order).
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-// Until the LDS reads so far have their data: what they read may be loaded over.
-__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-
 __device__ __forceinline__ float half_of(const uint32_t* w, int i) {
   return f16_bits_to_f32((uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]));
 }
@@ -314,7 +296,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES)) void attn_decode_kern
   constexpr int kJoin = (kWaves - 1) * S::TILES * 64 * 16;
   __shared__ __align__(16) uint8_t s_ring[kWaves * 2 * S::SLOT > kJoin ? kWaves * 2 * S::SLOT : kJoin];
   uint8_t* const ring = s_ring + wave * (2 * S::SLOT);
-  const uint32_t ring_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)ring);
+  const uint32_t ring_at = __builtin_amdgcn_readfirstlane(lds_address(ring));
   const auto* table = (const __attribute__((address_space(4))) int32_t*)(a.table + (int64_t)b * a.table_stride);
   const int steps = (k1 - k0 + kTile - 1) / kTile;
   const int mine = steps > wave ? (steps - wave + kWaves - 1) / kWaves : 0;
@@ -340,7 +322,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES)) void attn_decode_kern
       for (int i = 0; i < S::LOADS; ++i) {
         const uint32_t offset = S::SWIZZLE && keys ? swizzled_offset<FMT, NB>(lane, i) : (uint32_t)(16 * lane + 1024 * i);
         if (1024 * (i + 1) <= S::GROUP || 16 * lane + 1024 * i < S::GROUP)
-          load_to_lds(reinterpret_cast<const uint8_t*>(codes) + (u ? row_b : row_a) * S::ROW, offset, at + u * S::GROUP + 1024 * i);
+          load_once_to_lds(reinterpret_cast<const uint8_t*>(codes) + (u ? row_b : row_a) * S::ROW, offset, at + u * S::GROUP + 1024 * i);
       }
   };
   const auto load_keys = [&](uint32_t at) __attribute__((always_inline)) {
@@ -351,7 +333,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES)) void attn_decode_kern
       const uint8_t* kd = reinterpret_cast<const uint8_t*>(a.c.k_d);
       const int64_t row = (which & 1) ? row_b : row_a;
       const uint8_t* p = (which & 2 ? reinterpret_cast<const uint8_t*>(a.c.v_d) : kd) + row * (2 * NB) + 16 * i;
-      if (lane < 8 * NB) load_to_lds_far(p, at + 4 * S::GROUP);
+      if (lane < 8 * NB) load_once_to_lds_far(p, at + 4 * S::GROUP);
     }
   };
   const auto load_values = [&](uint32_t at) __attribute__((always_inline)) { load_rows(a.c.v, at + 2 * S::GROUP, false); };

@@ -122,6 +122,47 @@ __device__ __forceinline__ floatx16 mfma32(const Frag& a, const Frag& b, floatx1
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, x), __builtin_bit_cast(bf16x8_t, y), c, 0, 0, 0);
 }
 
+// LDS address of a shared array's element.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+// 16 bytes a lane from base + offset straight into LDS, lane after lane from `lds` on; the
+// second form for what is read once (non-temporal), the third from an address a lane.  In
+// assembly because the compiler, which cannot tell one part of LDS from another, waits for
+// every such load before any LDS read; here the waits are written out (wait_loads).
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void load_once_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(offset), "s"(base), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void load_once_to_lds_far(const uint8_t* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(p), "s"(lds) : "memory", "m0");
+}
+// Until at most N of the wavefront's loads are on their way (they come back in order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Until the LDS reads so far have their data: what they read may be loaded over.
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// Four rows' 16-bit elements of one column: of each 16 lanes, lanes 4 r .. 4 r + 3 give 32
+// contiguous bytes of row r (8 a lane), and lane c gets column c of the four rows.
+__device__ __forceinline__ u32x2 read_transposed(const uint8_t* p) {
+  typedef short short4_t __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4_t*)p));
+}
+
+// c + both elements of a 16-bit pair, in float32
+template <typename T>
+__device__ __forceinline__ float add_pair(uint32_t v, float c) {
+  if constexpr (__is_same(T, _Float16))
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, v), half2_t{(_Float16)1.0f, (_Float16)1.0f}, c, false);
+  else
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, v), bf16x2_t{(__bf16)1.0f, (__bf16)1.0f}, c, false);
+}
+
 // 2^x (v_exp_f32: about one unit in the last place; results below the normal range are 0)
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 

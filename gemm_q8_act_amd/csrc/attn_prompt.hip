@@ -15,10 +15,14 @@
 
 namespace nvq {
 
+// Every query tile of every head; a multiple of the chip's parts (find_place).
+int64_t attn_prompt_groups(int64_t B, int64_t Tq, int64_t Hq) { return ((Tq / 128 + B) * Hq + 7) / 8 * 8; }
+
 namespace {
 
 constexpr int kWaves = 4;
 constexpr int kQueries = 32 * kWaves;
+constexpr int kKeys = 64;  // of a tile
 constexpr float kSlack = 8.0f;
 
 struct PromptArgs {
@@ -33,6 +37,29 @@ struct PromptArgs {
   int causal;
 
 };
+
+// Which head and which query tile (of all sequences) a workgroup takes.  Workgroups go round the
+// chip's 8 dies, each with an L2 of its own, so the query heads of a key head stay on one die
+// (or, with fewer than 8 key heads, on as few as there are): its keys and values are read into
+// one L2.  Tiles in rising order on every die; find_span counts them from the long ones.
+struct Place {
+  int head, tile;
+};
+__device__ __forceinline__ Place find_place(const PromptArgs& a) {
+  const int x = (int)blockIdx.x % 8, r = (int)blockIdx.x / 8;
+  int kvh, g, tile;
+  if (a.Hkv % 8 == 0) {
+    const int heads = a.G * (a.Hkv / 8), i = r % heads;
+    tile = r / heads, kvh = x + 8 * (i / a.G), g = i % a.G;
+  } else if (8 % a.Hkv == 0) {
+    const int i = r * (8 / a.Hkv) + x / a.Hkv;
+    tile = i / a.G, kvh = x % a.Hkv, g = i % a.G;
+  } else {
+    tile = (int)blockIdx.x / a.Hq;
+    return {(int)blockIdx.x % a.Hq, tile};
+  }
+  return {kvh * a.G + g, tile};
+}
 
 struct Span {
   int q0, m, k0, n;  // the sequence's first query and number of them, and keys
@@ -73,20 +100,46 @@ __device__ __forceinline__ bool find_span(const PromptArgs& a, int want, Span& s
   return false;
 }
 
+// A staged tile of 64 key (or value) rows: where its 16-byte pieces sit.  The rows follow one
+// another; within a row the pieces are exchanged by row bits, so that the lanes of one LDS
+// read, which take one piece of different rows (keys), or 32 bytes of each of four rows
+// (values, transposed), fall on different banks (64 of 4 bytes).
+template <int NB>
+struct Stage {
+  static constexpr int ROW = 64 * NB, PIECES = 4 * NB, BYTES = kKeys * ROW;
+  static constexpr int LOADS = BYTES / 1024 / kWaves;  // 1 KB loads of a wavefront
+  static __device__ __forceinline__ int key_piece(int row, int i) {
+    if constexpr (PIECES == 16 || PIECES == 32) return i ^ (row & 15);
+    if constexpr (PIECES == 8) return i ^ ((row >> 1) & 7);
+    if constexpr (PIECES == 4) return i ^ ((row >> 2) & 3);
+    return i;
+  }
+  static __device__ __forceinline__ int value_piece(int row, int i) {
+    if constexpr (PIECES == 16 || PIECES == 32) return i ^ ((row & 3) << 2);
+    if constexpr (PIECES == 8) return i ^ ((row & 2) << 1);
+    return i;
+  }
+};
+
 template <typename T, int NB>
-__global__ __launch_bounds__(64 * kWaves) void attn_prompt_kernel(PromptArgs a) {
-  constexpr int D = 32 * NB, TK = NB <= 4 ? 64 : 32, KB = TK / 32;
-  constexpr int ROW = D + 8;  // halves of a staged row
-  __shared__ uint16_t s_k[TK * ROW], s_v[TK * ROW];
+__global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kernel(PromptArgs a) {
+  typedef Stage<NB> S;
+  __shared__ __align__(16) uint8_t s_keys[2 * S::BYTES], s_values[2 * S::BYTES];
   const int tid = (int)threadIdx.x, lane = tid & 63, c = lane & 31, hi = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int head = (int)blockIdx.x % a.Hq, kvh = head / a.G;
+  const Place place = find_place(a);
   Span sp;
-  if (!find_span(a, (int)blockIdx.x / a.Hq, sp)) return;
-  const int i0 = sp.tile * kQueries, iw = i0 + 32 * wave, i = iw + c;  // this lane's query
+  if (!find_span(a, place.tile, sp)) return;
+  const int head = place.head, kvh = head / a.G;
+  const int i0 = sp.tile * kQueries, iw = i0 + 32 * wave, i = iw + c;  // the block's and the wavefront's first query, the lane's
   const int shift = sp.n - sp.m;
-  const int limit = a.causal ? min(i + shift, sp.n - 1) : sp.n - 1;  // the last key it sees, -1 or less: none
+  const int limit = a.causal ? min(i + shift, sp.n - 1) : sp.n - 1;  // the last key it sees; below 0: none
+  // keys that the block's and the wavefront's last query see, in tiles
   const int end = a.causal ? min(sp.n, min(i0 + kQueries, sp.m) + shift) : sp.n;
+  const int end_w = iw >= sp.m ? 0 : a.causal ? min(sp.n, min(iw + 32, sp.m) + shift) : sp.n;
+  const int tiles = end > 0 ? (end + kKeys - 1) / kKeys : 0, mine = end_w > 0 ? (end_w + kKeys - 1) / kKeys : 0;
+  // from here on a tile has keys that some of the wavefront's queries do not see
+  const int whole = (a.causal ? min(sp.n, max(iw + shift + 1, 0)) : sp.n) / kKeys;
 
   Frag qf[2 * NB];
   {
@@ -98,88 +151,143 @@ __global__ __launch_bounds__(64 * kWaves) void attn_prompt_kernel(PromptArgs a) 
       for (int j = 0; j < 4; ++j) qf[ks].v[j] = w[j] ^ a.flip;
     }
   }
+
+  // Tiles on their way into LDS: load j of the wavefront takes 64 pieces, one a lane, in LDS order.
+  const uint8_t* keys = reinterpret_cast<const uint8_t*>(a.k + (int64_t)sp.k0 * a.k_t + (int64_t)kvh * a.k_h);
+  const uint8_t* values = reinterpret_cast<const uint8_t*>(a.v + (int64_t)sp.k0 * a.v_t + (int64_t)kvh * a.v_h);
+  const uint32_t keys_at = lds_address(s_keys), values_at = lds_address(s_values);
+  // slot: t % 2, known where it is called
+  const auto load_tile = [&](const uint8_t* base, int64_t stride, bool is_key, int t, uint32_t at) __attribute__((always_inline)) {
+    const uint8_t* first = base + (int64_t)t * kKeys * stride * 2;
+    const int last = sp.n - 1 - t * kKeys;  // rows past the sequence's end are its last one again
+#pragma unroll
+    for (int j = 0; j < S::LOADS; ++j) {
+      const int id = (wave * S::LOADS + j) * 64 + lane, row = id / S::PIECES, pos = id % S::PIECES;
+      const uint32_t offset = (uint32_t)min(row, last) * (uint32_t)(2 * stride) + 16 * (is_key ? S::key_piece(row, pos) : S::value_piece(row, pos));
+      load_to_lds(first, offset, at + (uint32_t)((wave * S::LOADS + j) * 1024));
+    }
+  };
+  const auto load_keys = [&](int t, int slot) __attribute__((always_inline)) {
+    if (t < tiles) load_tile(keys, a.k_t, true, t, keys_at + slot * S::BYTES);
+  };
+  const auto load_values = [&](int t, int slot) __attribute__((always_inline)) {
+    if (t < tiles) load_tile(values, a.v_t, false, t, values_at + slot * S::BYTES);
+  };
+
   floatx16 acc[NB];
 #pragma unroll
   for (int t = 0; t < NB; ++t)
 #pragma unroll
     for (int j = 0; j < 16; ++j) acc[t][j] = 0.0f;
-  float m = -__builtin_inff(), l = 0.0f;
-  const uint16_t* kb = a.k + (int64_t)sp.k0 * a.k_t + (int64_t)kvh * a.k_h;
-  const uint16_t* vb = a.v + (int64_t)sp.k0 * a.v_t + (int64_t)kvh * a.v_h;
+  float m = -__builtin_inff(), l = 0.0f, top = -__builtin_inff();
 
-  for (int kt = 0; kt < end; kt += TK) {
-    __syncthreads();
+  // S^T of the tile in a slot
+  const auto scores = [&](int slot, floatx16 (&s)[2]) __attribute__((always_inline)) {
+    const uint8_t* tile = s_keys + slot * S::BYTES;
 #pragma unroll
-    for (int u = 0; u < (TK * 4 * NB + 255) / 256; ++u) {
-      const int id = u * 256 + tid, r = id / (4 * NB), ch = id % (4 * NB);
-      if (TK * 4 * NB % 256 != 0 && id >= TK * 4 * NB) break;
-      const int key = min(kt + r, sp.n - 1);
-      *reinterpret_cast<u32x4*>(s_k + r * ROW + 8 * ch) = *reinterpret_cast<const u32x4*>(kb + (int64_t)key * a.k_t + 8 * ch);
-      *reinterpret_cast<u32x4*>(s_v + r * ROW + 8 * ch) = *reinterpret_cast<const u32x4*>(vb + (int64_t)key * a.v_t + 8 * ch);
-    }
-    __syncthreads();
-    floatx16 s[KB];
+    for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) s[b][j] = 0.0f;
+      for (int j = 0; j < 16; ++j) s[kb][j] = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < 2 * NB; ++ks) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(s_k + (32 * b + c) * ROW + 16 * ks + 8 * hi);
-        s[b] = mfma32<T>(Frag{w[0], w[1], w[2], w[3]}, qf[ks], s[b]);
+        const int row = 32 * kb + c;
+        const u32x4 w = *reinterpret_cast<const u32x4*>(tile + row * S::ROW + 16 * S::key_piece(row, 2 * ks + hi));
+        s[kb] = mfma32<T>(Frag{w[0], w[1], w[2], w[3]}, qf[ks], s[kb]);
       }
     }
-    if (kt + TK - 1 > (a.causal ? iw + shift : sp.n - 1) || kt + TK > sp.n) {
+  };
+  // Tile t: no score for keys that the query does not see; then its largest (the lane's part)
+  const auto finish_scores = [&](int t, floatx16 (&s)[2]) __attribute__((always_inline)) {
+    if (t >= whole) {
 #pragma unroll
-      for (int b = 0; b < KB; ++b)
+      for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          if (kt + 32 * b + 8 * (j >> 2) + 4 * hi + (j & 3) > limit) s[b][j] = -__builtin_inff();
+          if (t * kKeys + 32 * kb + 8 * (j >> 2) + 4 * hi + (j & 3) > limit) s[kb][j] = -__builtin_inff();
     }
-    float top = s[0][0];
+    float x = s[0][0];
 #pragma unroll
-    for (int b = 0; b < KB; ++b)
+    for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) top = fmaxf(top, s[b][j]);
-    top *= a.scale_log2;
+      for (int j = 0; j < 16; ++j) x = fmaxf(x, s[kb][j]);
+    top = x * a.scale_log2;
+  };
+  // Tile t in `slot`: its probabilities and their product with the values, and the next tile's
+  // scores, which depend on neither
+  const auto step = [&](int t, int slot, floatx16 (&s)[2], floatx16 (&next)[2]) __attribute__((always_inline)) {
     if (__any(top > m + kSlack)) {
       const float m_new = fmaxf(m, max_32(top));
       const float f = m_new == -__builtin_inff() ? 1.0f : exp2_fast(m - m_new);
       l *= f;
 #pragma unroll
-      for (int t = 0; t < NB; ++t) acc[t] *= f;
+      for (int d = 0; d < NB; ++d) acc[d] *= f;
       m = m_new;
     }
+    scores(slot ^ 1, next);
     const float m_safe = m == -__builtin_inff() ? 0.0f : m;
+    Frag pf[2][2];
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
+    for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        s[b][j] = exp2_fast(__builtin_fmaf(s[b][j], a.scale_log2, -m_safe));
-        l += s[b][j];
-      }
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        Frag pf;
+        for (int j = 0; j < 4; ++j) {
+          const float x = exp2_fast(__builtin_fmaf(s[kb][8 * h + 2 * j], a.scale_log2, -m_safe));
+          const float y = exp2_fast(__builtin_fmaf(s[kb][8 * h + 2 * j + 1], a.scale_log2, -m_safe));
+          pf[kb][h].v[j] = pack_pair<T>(x, y);
+          l = add_pair<T>(pf[kb][h].v[j], l);
+        }
+    const uint8_t* tile = s_values + slot * S::BYTES;
+    const int jj = lane & 15, row_in = 4 * hi + (jj >> 2), half = (lane >> 4) & 1;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pf.v[j] = pack_pair<T>(s[b][8 * t + 2 * j], s[b][8 * t + 2 * j + 1]);
+    for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int dt = 0; dt < NB; ++dt) {
-          Frag vf;
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int d = 0; d < NB; ++d) {
+          Frag f;
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const int jj = lane & 15, gg = lane >> 4;
-            typedef short s4 __attribute__((ext_vector_type(4)));
-            const uint16_t* p = s_v + (32 * b + 16 * t + 8 * r + 4 * hi + (jj >> 2)) * ROW + 32 * dt + 16 * (gg & 1) + 4 * (jj & 3);
-            const s4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)p);
-            const u32x2 x = __builtin_bit_cast(u32x2, w);
-            vf.v[2 * r] = x[0], vf.v[2 * r + 1] = x[1];
+            const int row = 32 * kb + 16 * h + 8 * r + row_in;
+            const u32x2 x = read_transposed(tile + row * S::ROW + 16 * S::value_piece(row, 4 * d + 2 * half + ((jj & 3) >> 1)) + 8 * (jj & 1));
+            f.v[2 * r] = x[0], f.v[2 * r + 1] = x[1];
           }
-          acc[dt] = mfma32<T>(vf, pf, acc[dt]);
+          acc[d] = mfma32<T>(f, pf[kb][h], acc[d]);
         }
-      }
+    finish_scores(t + 1, next);
+  };
+
+  // Before tile t's step: its values and the next tile's keys are there, and everyone is done
+  // with the slots that the next loads go to.
+  const auto turn = [&](int t, int slot) __attribute__((always_inline)) {
+    wait_loads<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    load_values(t + 1, slot ^ 1);
+    load_keys(t + 2, slot);
+  };
+  floatx16 sa[2], sb[2];
+  if (tiles > 0) {
+    load_keys(0, 0);
+    load_values(0, 0);
+    load_keys(1, 1);
+    wait_loads<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (mine > 0) {
+      scores(0, sa);
+      finish_scores(0, sa);
+    }
+    for (int t = 0;;) {
+      turn(t, 0);
+      if (t < mine) step(t, 0, sa, sb);
+      if (++t >= tiles) break;
+      turn(t, 1);
+      if (t < mine) step(t, 1, sb, sa);
+      if (++t >= tiles) break;
     }
   }
+
   l = sum_32(l);
   if (i >= sp.m) return;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a query that sees no key gives zeros
@@ -192,25 +300,26 @@ __global__ __launch_bounds__(64 * kWaves) void attn_prompt_kernel(PromptArgs a) 
           u32x2{pack_pair<T>(acc[t][4 * j] * inv, acc[t][4 * j + 1] * inv), pack_pair<T>(acc[t][4 * j + 2] * inv, acc[t][4 * j + 3] * inv)};
 }
 
-template <typename T>
-hipError_t launch_type(const PromptArgs& a, int nb, int64_t blocks, hipStream_t s) {
-  const dim3 grid((unsigned)blocks), block(64 * kWaves);
-  switch (nb) {
-    case 1: hipLaunchKernelGGL((attn_prompt_kernel<T, 1>), grid, block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((attn_prompt_kernel<T, 2>), grid, block, 0, s, a); break;
-    case 3: hipLaunchKernelGGL((attn_prompt_kernel<T, 3>), grid, block, 0, s, a); break;
-    case 4: hipLaunchKernelGGL((attn_prompt_kernel<T, 4>), grid, block, 0, s, a); break;
-    case 5: hipLaunchKernelGGL((attn_prompt_kernel<T, 5>), grid, block, 0, s, a); break;
-    case 6: hipLaunchKernelGGL((attn_prompt_kernel<T, 6>), grid, block, 0, s, a); break;
-    case 7: hipLaunchKernelGGL((attn_prompt_kernel<T, 7>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((attn_prompt_kernel<T, 8>), grid, block, 0, s, a); break;
-  }
+template <typename T, int NB>
+hipError_t launch_nb(const PromptArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((attn_prompt_kernel<T, NB>), dim3((unsigned)attn_prompt_groups(a.B, a.Tq, a.Hq)), dim3(64 * kWaves), 0, s, a);
   return hipGetLastError();
+}
+template <typename T>
+hipError_t launch_type(const PromptArgs& a, int nb, hipStream_t s) {
+  switch (nb) {
+    case 1: return launch_nb<T, 1>(a, s);
+    case 2: return launch_nb<T, 2>(a, s);
+    case 3: return launch_nb<T, 3>(a, s);
+    case 4: return launch_nb<T, 4>(a, s);
+    case 5: return launch_nb<T, 5>(a, s);
+    case 6: return launch_nb<T, 6>(a, s);
+    case 7: return launch_nb<T, 7>(a, s);
+    default: return launch_nb<T, 8>(a, s);
+  }
 }
 
 }  // namespace
-
-int64_t attn_prompt_groups(int64_t B, int64_t Tq, int64_t Hq) { return (Tq / kQueries + B) * Hq; }
 
 hipError_t launch_attn_prompt(int type, const void* q, const void* k, const void* v, void* out, const int64_t strides[8],
                               const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,
@@ -228,9 +337,8 @@ hipError_t launch_attn_prompt(int type, const void* q, const void* k, const void
   a.flip = __builtin_signbit(scale) ? 0x80008000u : 0u;
   a.causal = causal;
 
-  const int64_t blocks = attn_prompt_groups(B, Tq, Hq);
-  if (type == NVQ_TYPE_F16) return launch_type<_Float16>(a, (int)(D / 32), blocks, stream);
-  return launch_type<__bf16>(a, (int)(D / 32), blocks, stream);
+  if (type == NVQ_TYPE_F16) return launch_type<_Float16>(a, (int)(D / 32), stream);
+  return launch_type<__bf16>(a, (int)(D / 32), stream);
 }
 
 }  // namespace nvq
