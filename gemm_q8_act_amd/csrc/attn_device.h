@@ -139,6 +139,16 @@ __device__ __forceinline__ void load_once_to_lds(const uint8_t* base, uint32_t o
 __device__ __forceinline__ void load_once_to_lds_far(const uint8_t* p, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(p), "s"(lds) : "memory", "m0");
 }
+// The first `bytes` bytes from p on as a buffer: loads past its end give zeros.
+__device__ __forceinline__ u32x4 buffer_of(const void* p, uint32_t bytes) {
+  const uint64_t at = (uint64_t)p;
+  return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, bytes, 0x00020000u};
+}
+// 16 bytes a lane from the buffer at `offset` into LDS, as above.  Orders itself with waits and
+// barriers only: it may move among the LDS reads of other slots.
+__device__ __forceinline__ void buffer_to_lds(u32x4 buffer, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(buffer), "s"(lds) : "m0");
+}
 // Until at most N of the wavefront's loads are on their way (they come back in order).
 template <int N>
 __device__ __forceinline__ void wait_loads() {

@@ -121,6 +121,7 @@ struct Stage {
   }
 };
 
+
 template <typename T, int NB>
 __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kernel(PromptArgs a) {
   typedef Stage<NB> S;
@@ -152,26 +153,22 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
     }
   }
 
-  // Tiles on their way into LDS: load j of the wavefront takes 64 pieces, one a lane, in LDS order.
-  const uint8_t* keys = reinterpret_cast<const uint8_t*>(a.k + (int64_t)sp.k0 * a.k_t + (int64_t)kvh * a.k_h);
-  const uint8_t* values = reinterpret_cast<const uint8_t*>(a.v + (int64_t)sp.k0 * a.v_t + (int64_t)kvh * a.v_h);
-  const uint32_t keys_at = lds_address(s_keys), values_at = lds_address(s_values);
-  // slot: t % 2, known where it is called
-  const auto load_tile = [&](const uint8_t* base, int64_t stride, bool is_key, int t, uint32_t at) __attribute__((always_inline)) {
-    const uint8_t* first = base + (int64_t)t * kKeys * stride * 2;
-    const int last = sp.n - 1 - t * kKeys;  // rows past the sequence's end are its last one again
+  // Tiles on their way into LDS: load j of the wavefront takes 64 pieces, one a lane, in LDS
+  // order.  A tile's descriptor ends behind the sequence's last row: what a load asks for past
+  // it comes as zeros (and nothing is read), the same for whole tiles past the end.
+  uint32_t key_from[S::LOADS], value_from[S::LOADS];
 #pragma unroll
-    for (int j = 0; j < S::LOADS; ++j) {
-      const int id = (wave * S::LOADS + j) * 64 + lane, row = id / S::PIECES, pos = id % S::PIECES;
-      const uint32_t offset = (uint32_t)min(row, last) * (uint32_t)(2 * stride) + 16 * (is_key ? S::key_piece(row, pos) : S::value_piece(row, pos));
-      load_to_lds(first, offset, at + (uint32_t)((wave * S::LOADS + j) * 1024));
-    }
-  };
-  const auto load_keys = [&](int t, int slot) __attribute__((always_inline)) {
-    if (t < tiles) load_tile(keys, a.k_t, true, t, keys_at + slot * S::BYTES);
-  };
-  const auto load_values = [&](int t, int slot) __attribute__((always_inline)) {
-    if (t < tiles) load_tile(values, a.v_t, false, t, values_at + slot * S::BYTES);
+  for (int j = 0; j < S::LOADS; ++j) {
+    const int id = (wave * S::LOADS + j) * 64 + lane, row = id / S::PIECES, pos = id % S::PIECES;
+    key_from[j] = (uint32_t)row * (uint32_t)(2 * a.k_t) + 16 * S::key_piece(row, pos);
+    value_from[j] = (uint32_t)row * (uint32_t)(2 * a.v_t) + 16 * S::value_piece(row, pos);
+  }
+  const uint32_t keys_at = lds_address(s_keys) + (uint32_t)(wave * S::LOADS * 1024);
+  const uint32_t values_at = lds_address(s_values) + (uint32_t)(wave * S::LOADS * 1024);
+  const auto tile_of = [&](const uint16_t* p, int64_t stride_t, int64_t stride_h, int t) __attribute__((always_inline)) {
+    const int rows = min(sp.n - t * kKeys, kKeys);
+    return buffer_of(p + ((int64_t)sp.k0 + (int64_t)t * kKeys) * stride_t + (int64_t)kvh * stride_h,
+                     rows > 0 ? (uint32_t)(rows - 1) * (uint32_t)(2 * stride_t) + S::ROW : 0u);
   };
 
   floatx16 acc[NB];
@@ -181,8 +178,18 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
     for (int j = 0; j < 16; ++j) acc[t][j] = 0.0f;
   float m = -__builtin_inff(), l = 0.0f, top = -__builtin_inff();
 
-  // S^T of the tile in a slot
-  const auto scores = [&](int slot, floatx16 (&s)[2]) __attribute__((always_inline)) {
+  uint32_t key_offset[2 * NB], value_offset[NB];
+#pragma unroll
+  for (int ks = 0; ks < 2 * NB; ++ks) key_offset[ks] = in_vgpr((uint32_t)(c * S::ROW + 16 * S::key_piece(c, 2 * ks + hi)));
+  {
+    const int jj = lane & 15, row_in = 4 * hi + (jj >> 2), half = (lane >> 4) & 1;
+#pragma unroll
+    for (int d = 0; d < NB; ++d)
+      value_offset[d] = in_vgpr((uint32_t)(row_in * S::ROW + 16 * S::value_piece(row_in, 4 * d + 2 * half + ((jj & 3) >> 1)) + 8 * (jj & 1)));
+  }
+  // S^T of the tile in a slot; between the products, the loads of the values and keys that
+  // come next (one behind every second product, so that none waits for the others' issue)
+  const auto scores = [&](int slot, floatx16 (&s)[2], auto load) __attribute__((always_inline)) {
     const uint8_t* tile = s_keys + slot * S::BYTES;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
@@ -190,13 +197,21 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
       for (int j = 0; j < 16; ++j) s[kb][j] = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < 2 * NB; ++ks) {
-        const int row = 32 * kb + c;
-        const u32x4 w = *reinterpret_cast<const u32x4*>(tile + row * S::ROW + 16 * S::key_piece(row, 2 * ks + hi));
+        const u32x4 w = *reinterpret_cast<const u32x4*>(tile + key_offset[ks] + 32 * kb * S::ROW);
         s[kb] = mfma32<T>(Frag{w[0], w[1], w[2], w[3]}, qf[ks], s[kb]);
+        if (ks % 2) load(kb * NB + ks / 2);
       }
     }
   };
   // Tile t: no score for keys that the query does not see; then its largest (the lane's part)
+  const auto largest = [&](floatx16 (&s)[2]) __attribute__((always_inline)) {
+    float x = s[0][0];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x = fmaxf(x, s[kb][j]);
+    top = x * a.scale_log2;
+  };
   const auto finish_scores = [&](int t, floatx16 (&s)[2]) __attribute__((always_inline)) {
     if (t >= whole) {
 #pragma unroll
@@ -204,13 +219,8 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           if (t * kKeys + 32 * kb + 8 * (j >> 2) + 4 * hi + (j & 3) > limit) s[kb][j] = -__builtin_inff();
+      largest(s);
     }
-    float x = s[0][0];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) x = fmaxf(x, s[kb][j]);
-    top = x * a.scale_log2;
   };
   // Tile t in `slot`: its probabilities and their product with the values, and the next tile's
   // scores, which depend on neither
@@ -223,7 +233,13 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
       for (int d = 0; d < NB; ++d) acc[d] *= f;
       m = m_new;
     }
-    scores(slot ^ 1, next);
+    const u32x4 values = tile_of(a.v, a.v_t, a.v_h, t + 1), keys = tile_of(a.k, a.k_t, a.k_h, t + 2);
+    scores(slot ^ 1, next, [&](int j) __attribute__((always_inline)) {
+      if (j < S::LOADS)
+        buffer_to_lds(values, value_from[j], values_at + (slot ^ 1) * S::BYTES + 1024 * j);
+      else
+        buffer_to_lds(keys, key_from[j - S::LOADS], keys_at + slot * S::BYTES + 1024 * (j - S::LOADS));
+    });
     const float m_safe = m == -__builtin_inff() ? 0.0f : m;
     Frag pf[2][2];
 #pragma unroll
@@ -238,7 +254,6 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
           l = add_pair<T>(pf[kb][h].v[j], l);
         }
     const uint8_t* tile = s_values + slot * S::BYTES;
-    const int jj = lane & 15, row_in = 4 * hi + (jj >> 2), half = (lane >> 4) & 1;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -248,44 +263,60 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
           Frag f;
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const int row = 32 * kb + 16 * h + 8 * r + row_in;
-            const u32x2 x = read_transposed(tile + row * S::ROW + 16 * S::value_piece(row, 4 * d + 2 * half + ((jj & 3) >> 1)) + 8 * (jj & 1));
+            const u32x2 x = read_transposed(tile + value_offset[d] + (32 * kb + 16 * h + 8 * r) * S::ROW);
             f.v[2 * r] = x[0], f.v[2 * r + 1] = x[1];
           }
           acc[d] = mfma32<T>(f, pf[kb][h], acc[d]);
         }
+    largest(next);
     finish_scores(t + 1, next);
   };
 
   // Before tile t's step: its values and the next tile's keys are there, and everyone is done
-  // with the slots that the next loads go to.
-  const auto turn = [&](int t, int slot) __attribute__((always_inline)) {
+  // with the slots that the step's loads go to.  Wavefronts with no query that sees the tile
+  // only load their share.
+  const auto turn = [&]() __attribute__((always_inline)) {
     wait_loads<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    load_values(t + 1, slot ^ 1);
-    load_keys(t + 2, slot);
+  };
+  const auto load_values = [&](int t, int slot) __attribute__((always_inline)) {
+    const u32x4 values = tile_of(a.v, a.v_t, a.v_h, t);
+#pragma unroll
+    for (int j = 0; j < S::LOADS; ++j) buffer_to_lds(values, value_from[j], values_at + slot * S::BYTES + 1024 * j);
+  };
+  const auto load_keys = [&](int t, int slot) __attribute__((always_inline)) {
+    const u32x4 keys = tile_of(a.k, a.k_t, a.k_h, t);
+#pragma unroll
+    for (int j = 0; j < S::LOADS; ++j) buffer_to_lds(keys, key_from[j], keys_at + slot * S::BYTES + 1024 * j);
   };
   floatx16 sa[2], sb[2];
   if (tiles > 0) {
     load_keys(0, 0);
     load_values(0, 0);
     load_keys(1, 1);
-    wait_loads<0>();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    turn();
     if (mine > 0) {
-      scores(0, sa);
+      scores(0, sa, [](int) __attribute__((always_inline)) {});
+      largest(sa);
       finish_scores(0, sa);
     }
+    const auto pass = [&](int t, int slot, floatx16 (&s)[2], floatx16 (&next)[2]) __attribute__((always_inline)) {
+      turn();
+      if (t < mine) {
+        step(t, slot, s, next);
+      } else {
+        load_values(t + 1, slot ^ 1);
+        load_keys(t + 2, slot);
+      }
+    };
     for (int t = 0;;) {
-      turn(t, 0);
-      if (t < mine) step(t, 0, sa, sb);
+      pass(t, 0, sa, sb);
       if (++t >= tiles) break;
-      turn(t, 1);
-      if (t < mine) step(t, 1, sb, sa);
+      pass(t, 1, sb, sa);
       if (++t >= tiles) break;
     }
+    wait_loads<0>();  // (zeros for tiles past the end): LDS is another workgroup's next
   }
 
   l = sum_32(l);
