@@ -624,23 +624,25 @@ def nvq_debug_isums(fmt: int, path: int, w, q, N: int, isums, stream=None) -> No
 # ---------------------------------------------------------------------------
 
 # A decode step makes these calls with a few microseconds of work each, so the checks below
-# compare shapes and types directly and say more only once something is wrong.
+# compare types and shapes directly and say more only once something is wrong.
+_torch = None            # set with the tables
 _row_types: dict = {}    # torch dtype -> NVQ_TYPE_*
 _cache_types: dict = {}  # torch dtype -> NVQ_KV_*
 
 
 def _attn_lib():
-    if not _row_types:
-        import torch
+    global _torch
+    import torch
 
-        _row_types.update({torch.float32: NVQ_TYPE_F32, torch.float16: NVQ_TYPE_F16, torch.bfloat16: NVQ_TYPE_BF16})
-        _cache_types.update({torch.int8: NVQ_KV_Q8_0, torch.float16: NVQ_KV_F16, torch.bfloat16: NVQ_KV_BF16})
-    return _lib or lib()
+    _row_types.update({torch.float32: NVQ_TYPE_F32, torch.float16: NVQ_TYPE_F16, torch.bfloat16: NVQ_TYPE_BF16})
+    _cache_types.update({torch.int8: NVQ_KV_Q8_0, torch.float16: NVQ_KV_F16, torch.bfloat16: NVQ_KV_BF16})
+    _torch = torch
+    return lib()
 
 
 def _rows(t, dtype, shape, name):
     """A row tensor [rows, heads, D] whose channels are contiguous (its other strides are passed on): its strides."""
-    if t is None or t.dtype != dtype or t.shape != shape:
+    if t is None or t.dtype is not dtype or t.shape != shape:
         _need(t, dtype, shape, name)
     st = t.stride()
     if st[2] != 1 and shape[2] > 1:
@@ -649,7 +651,7 @@ def _rows(t, dtype, shape, name):
 
 
 def _dense(t, dtype, shape, name):
-    if t is None or t.dtype != dtype or t.shape != shape:
+    if t is None or t.dtype is not dtype or t.shape != shape:
         _need(t, dtype, shape, name)
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensors passed to libnvq must be contiguous")
@@ -665,45 +667,40 @@ def _row_shape(t, name):
 def _on_device(stream, *tensors):
     """Every tensor on the current GPU (pointers of another one must not reach a launch on this one's stream): the
     stream to launch on."""
-    import torch
-
-    here = torch.cuda.current_device()
+    here = _torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != here:
             raise ValueError(f"tensor on {t.device}, expected the current device cuda:{here}")
-    return torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream)
+    return _torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream)
 
 
 def _kv_cache(k_cache, v_cache, k_d, v_d):
-    """(format, shape, pointers) of a cache [n_pages, heads, page, D]."""
+    """(format, shape, the four pointers) of a cache [n_pages, heads, page, D]."""
     fmt = None if k_cache is None or k_cache.dim() != 4 else _cache_types.get(k_cache.dtype)
     if fmt is None:
         raise ValueError("k_cache: an int8 (Q8_0), float16 or bfloat16 tensor [n_pages, heads, page, D] is required")
     shape = k_cache.shape
-    p = [_dense(k_cache, k_cache.dtype, shape, "k_cache"), _dense(v_cache, k_cache.dtype, shape, "v_cache"), None, None]
+    kp, vp = _dense(k_cache, k_cache.dtype, shape, "k_cache"), _dense(v_cache, k_cache.dtype, shape, "v_cache")
     if fmt != NVQ_KV_Q8_0:
         if k_d is not None or v_d is not None:
             raise ValueError("k_d, v_d: a 16-bit cache has no scales")
-        return fmt, shape, p
-    d_shape = (shape[0], shape[1], shape[2], shape[3] // 32)
-    for i, t in ((2, k_d), (3, v_d)):
+        return fmt, shape, kp, vp, None, None
+    d_shape = (*shape[:3], shape[3] // 32)
+    for t in (k_d, v_d):
         if t is None or t.shape != d_shape or t.element_size() != 2 or not t.is_contiguous():
             raise ValueError("k_d and v_d must be contiguous 2-byte tensors [n_pages, heads, page, D/32]")
-        p[i] = t.data_ptr()
-    return fmt, shape, p
+    return fmt, shape, kp, vp, k_d.data_ptr(), v_d.data_ptr()
 
 
-def _kv_copy(name, k, v, slots, k_cache, v_cache, k_d, v_d, stream):
-    import torch
-
-    L = _attn_lib()
-    fmt, (n_pages, heads, page, D), p = _kv_cache(k_cache, v_cache, k_d, v_d)
-    shape = (_row_shape(k, "k")[0], heads, D)
-    ks, vs = _rows(k, k.dtype, shape, "k"), _rows(v, k.dtype, shape, "v")
-    sp = _dense(slots, torch.int64, shape[:1], "slots")
+def _kv_copy(fn, name, k, v, slots, k_cache, v_cache, k_d, v_d, stream):
+    fmt, (n_pages, heads, page, D), kp, vp, kdp, vdp = _kv_cache(k_cache, v_cache, k_d, v_d)
+    T = _row_shape(k, "k")[0]
+    dtype = k.dtype
+    ks, vs = _rows(k, dtype, (T, heads, D), "k"), _rows(v, dtype, (T, heads, D), "v")
+    sp = _dense(slots, _torch.int64, (T,), "slots")
     on = _on_device(stream, k, v, slots, k_cache, v_cache, k_d, v_d)
-    st = getattr(L, name)(fmt, _row_types[k.dtype], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], sp, shape[0], heads, D,
-                          p[0], p[1], p[2], p[3], n_pages, page, on)
+    st = fn(fmt, _row_types[dtype], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], sp, T, heads, D, kp, vp, kdp, vdp, n_pages,
+            page, on)
     if st:
         _check(st, name)
 
@@ -712,12 +709,14 @@ def nvq_kv_write(k, v, slots, k_cache, v_cache, k_d=None, v_d=None, stream=None)
     """Rows k, v [T, Hkv, D] (float32, float16 or bfloat16; token and head strides free) into a paged cache
     [n_pages, Hkv, page, D] at slots int64 [T] (page number * page + place; negative: none).  An int8 cache is
     Q8_0 and takes the binary16 scales k_d, v_d [n_pages, Hkv, page, D/32]; a 16-bit one takes none."""
-    _kv_copy("nvq_kv_write", k, v, slots, k_cache, v_cache, k_d, v_d, stream)
+    L = _lib if _torch is not None else _attn_lib()
+    _kv_copy(L.nvq_kv_write, "nvq_kv_write", k, v, slots, k_cache, v_cache, k_d, v_d, stream)
 
 
 def nvq_kv_read(k_cache, v_cache, slots, k, v, k_d=None, v_d=None, stream=None) -> None:
     """The cache rows at slots int64 [T] into k, v [T, Hkv, D] (arguments as nvq_kv_write's)."""
-    _kv_copy("nvq_kv_read", k, v, slots, k_cache, v_cache, k_d, v_d, stream)
+    L = _lib if _torch is not None else _attn_lib()
+    _kv_copy(L.nvq_kv_read, "nvq_kv_read", k, v, slots, k_cache, v_cache, k_d, v_d, stream)
 
 
 def nvq_attn_decode_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, max_pages: int, page: int) -> int:
@@ -728,24 +727,21 @@ def nvq_attn_decode(q, k_cache, v_cache, table, lengths, out, k_d=None, v_d=None
                     stream=None) -> None:
     """One new token per sequence: q [B, Hq, D] (strides free), the paged cache, table int32 [B, max_pages] and
     lengths int32 [B] -> out [B, Hq, D] of q's type.  scale: 1 / sqrt(D) unless given."""
-    import torch
-
-    L = _attn_lib()
-    fmt, (n_pages, heads, page, D), p = _kv_cache(k_cache, v_cache, k_d, v_d)
+    L = _lib if _torch is not None else _attn_lib()
+    fmt, (n_pages, heads, page, D), kp, vp, kdp, vdp = _kv_cache(k_cache, v_cache, k_d, v_d)
     B, Hq, _ = _row_shape(q, "q")
-    qs = _rows(q, q.dtype, (B, Hq, D), "q")
-    op = _dense(out, q.dtype, (B, Hq, D), "out")
+    dtype, shape = q.dtype, (B, Hq, D)
+    qs, op = _rows(q, dtype, shape, "q"), _dense(out, dtype, shape, "out")
     if table is None or table.dim() != 2:
         raise ValueError("table: int32 [B, max_pages] is required")
     max_pages = table.shape[1]
-    tp = _dense(table, torch.int32, (B, max_pages), "table")
-    lp = _dense(lengths, torch.int32, (B,), "lengths")
+    tp, lp = _dense(table, _torch.int32, (B, max_pages), "table"), _dense(lengths, _torch.int32, (B,), "lengths")
     on = _on_device(stream, q, k_cache, v_cache, table, lengths, out, k_d, v_d, workspace)
     if workspace is None:
         workspace = _workspace(L.nvq_attn_decode_workspace_bytes(B, Hq, heads, D, max_pages, page), stream, q)
     wp, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
-    st = L.nvq_attn_decode(fmt, _row_types[q.dtype], q.data_ptr(), qs[0], qs[1], B, Hq, heads, D, p[0], p[1], p[2], p[3], n_pages, page, tp,
-                           max_pages, lp, D ** -0.5 if scale is None else scale, op, wp, ws_bytes, on)
+    st = L.nvq_attn_decode(fmt, _row_types[dtype], q.data_ptr(), qs[0], qs[1], B, Hq, heads, D, kp, vp, kdp, vdp, n_pages, page, tp, max_pages, lp,
+                           D ** -0.5 if scale is None else scale, op, wp, ws_bytes, on)
     if st:
         _check(st, "nvq_attn_decode")
 
@@ -753,13 +749,11 @@ def nvq_attn_decode(q, k_cache, v_cache, table, lengths, out, k_d=None, v_d=None
 def _workspace(nbytes, stream, like):
     """Scratch of one call.  torch's allocator hands it out again in the order of the stream that it was allocated
     on, so on a stream of the caller's it has to be told of that one."""
-    import torch
-
     if not nbytes:
         return None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    if stream is not None and int(stream) != torch.cuda.current_stream(like.device).cuda_stream:
-        ws.record_stream(torch.cuda.ExternalStream(int(stream), device=like.device))
+    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=like.device)
+    if stream is not None and int(stream) != _torch.cuda.current_stream(like.device).cuda_stream:
+        ws.record_stream(_torch.cuda.ExternalStream(int(stream), device=like.device))
     return ws
 
 
@@ -767,9 +761,7 @@ def nvq_attn_prompt(q, k, v, cu_q, cu_k, out, scale=None, causal=True, stream=No
     """Packed prompts: q [Tq, Hq, D], k, v [Tk, Hkv, D] (float16 or bfloat16, strides free), cu_q, cu_k int32 [B+1]
     -> out [Tq, Hq, D] (strides free).  Query i of m sees keys j <= i + n - m of its n (causal), else all.
     scale: 1 / sqrt(D) unless given."""
-    import torch
-
-    L = _attn_lib()
+    L = _lib if _torch is not None else _attn_lib()
     Tq, Hq, D = _row_shape(q, "q")
     Tk, Hkv, _ = _row_shape(k, "k")
     t = q.dtype
@@ -777,7 +769,7 @@ def nvq_attn_prompt(q, k, v, cu_q, cu_k, out, scale=None, causal=True, stream=No
     os_ = _rows(out, t, (Tq, Hq, D), "out")
     if cu_q is None or cu_q.dim() != 1 or cu_q.shape[0] < 1:
         raise ValueError("cu_q: int32 [B + 1] is required")
-    cq, ck = _dense(cu_q, torch.int32, cu_q.shape, "cu_q"), _dense(cu_k, torch.int32, cu_q.shape, "cu_k")
+    cq, ck = _dense(cu_q, _torch.int32, cu_q.shape, "cu_q"), _dense(cu_k, _torch.int32, cu_q.shape, "cu_k")
     on = _on_device(stream, q, k, v, cu_q, cu_k, out)
     strides = _Strides(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
     st = L.nvq_attn_prompt(_row_types[t], q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), strides, cq, ck, cu_q.shape[0] - 1, Tq, Tk,

@@ -7,8 +7,8 @@
 // contiguous bytes a block, and the lane's codes are the 2 D/32 consecutive bytes that
 // the quantised row's element order gives it (nvq.h): one wide store.
 //
-// HBM-bound: D * (element bytes + 34/32) a row, each byte once.  Both tensors go in one
-// launch (blockIdx.y: keys, values): a decode step writes a few rows and is all launch.
+// HBM-bound: D * (element bytes + 34/32) a row, each byte once.  Keys and values go in one
+// launch: a decode step writes a few rows and is all launch.
 #include "attn_device.h"
 #include "nvq_launch.h"
 
@@ -22,7 +22,7 @@ struct KvArgs {
   uint8_t* codes[2];
   uint16_t* scales[2];
   const int64_t* slots;
-  int64_t n_rows;        // tokens * heads
+  int n_rows;            // tokens * heads
   int64_t n_slots;       // pages * page size
   uint32_t heads;
   uint32_t page_shift;
@@ -35,6 +35,31 @@ __device__ __forceinline__ uint32_t row16_umax(uint32_t v) {
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));
   return v;
+}
+
+// Q8_0 of a pair of a block whose largest magnitude's bits are `top`: its two codes, and the
+// block's binary16 scale.  The definition's IEEE divisions (amax / 127, x / d, ties to even)
+// come out bit for bit without their long instruction sequences, which bound the kernel:
+//   d: amax * fl(1/127) and one fma correction give fl(amax / 127) for every finite float.
+//   x / d: fma(x, rcp(d), 128) is within 4.2e-5 of 128 + fl(x / d) (one-ulp reciprocal, |x / d|
+//     <= 127.00002), so unless it lies within 2^-14 of a rounding tie its nearest whole number
+//     is the code + 128; nearer ones, and blocks whose reciprocal could leave the normal range,
+//     divide.
+// A block with an infinity or NaN takes a NaN scale: it reads back as NaN, never as numbers.
+__device__ __forceinline__ uint16_t quant_pair(const float (&x)[2], uint32_t top, uint16_t& scale) {
+  constexpr float kInv127 = 0x1.020408p-7f;  // fl(1 / 127)
+  const float amax = __builtin_bit_cast(float, top), t = amax * kInv127;
+  const float d = top < 0x7F800000u ? __builtin_fmaf(__builtin_fmaf(-t, 127.0f, amax), kInv127, t) : __builtin_nanf("");
+  const float r = d > 0.0f ? __builtin_amdgcn_rcpf(d) : 0.0f;
+  const float u0 = __builtin_fmaf(x[0], r, 128.0f), u1 = __builtin_fmaf(x[1], r, 128.0f);
+  float k0 = __builtin_rintf(u0), k1 = __builtin_rintf(u1);
+  if (fmaxf(fabsf(u0 - k0), fabsf(u1 - k1)) > 0.5f - 0x1.0p-14f || (d > 0.0f && d < 0x1.0p-100f)) {
+    k0 = fminf(fmaxf(__builtin_rintf(x[0] / d), -127.0f), 127.0f) + 128.0f;
+    k1 = fminf(fmaxf(__builtin_rintf(x[1] / d), -127.0f), 127.0f) + 128.0f;
+  }
+  const uint32_t codes = __builtin_amdgcn_cvt_pk_u8_f32(k1, 1u, __builtin_amdgcn_cvt_pk_u8_f32(k0, 0u, 0u));
+  scale = __builtin_bit_cast(uint16_t, (_Float16)d);
+  return (uint16_t)(codes ^ 0x8080u);
 }
 
 // N 16-bit pieces moved with the widest accesses that their common alignment allows (the
@@ -88,95 +113,104 @@ __device__ __forceinline__ void load_halves(const void* p, uint16_t (&v)[N]) {
 struct KvRow {
   int64_t t, h, cache;
 };
-__device__ __forceinline__ KvRow locate(const KvArgs& a, int64_t r) {
+__device__ __forceinline__ KvRow locate(const KvArgs& a, int r) {
   KvRow o;
-  // 32-bit division where the row number allows it
-  if (a.n_rows <= 0xFFFFFFFFll) {
-    const uint32_t t = (uint32_t)r / a.heads;
-    o.t = t, o.h = (uint32_t)r - t * a.heads;
-  } else {
-    o.t = r / a.heads, o.h = r - o.t * a.heads;
-  }
+  const uint32_t t = (uint32_t)r / a.heads;
+  o.t = t, o.h = (uint32_t)r - t * a.heads;
   const int64_t s = a.slots[o.t];
   const int64_t pg = s >> a.page_shift, off = s & ((1ll << a.page_shift) - 1);
   o.cache = s < 0 ? -1 : s >= a.n_slots ? -2 : ((pg * a.heads + o.h) << a.page_shift) + off;
   return o;
 }
 
-// T: the rows' type.  FMT: the cache's.  NB: 32-blocks of a row.
+template <typename T>
+__device__ __forceinline__ const T* row_at(const KvArgs& a, const KvRow& row, int w) {
+  return reinterpret_cast<const T*>(a.rows[w]) + row.t * a.stride_t[w] + row.h * a.stride_h[w] + 2 * (threadIdx.x & 15);
+}
+
+// T: the rows' type.  FMT: the cache's.  NB: 32-blocks of a row.  16 lanes take a token's key row
+// and value row of one head; all loads go out before the slot is looked at (the rows are there
+// whatever it says), so one round trip to memory covers both.
 template <typename T, int FMT, int NB>
 __global__ __launch_bounds__(256) void kv_write_kernel(KvArgs a) {
-  const int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int r = (int)blockIdx.x * 16 + (int)(threadIdx.x >> 4);
   if (r >= a.n_rows) return;  // whole 16-lane rows leave together
-  const int n = (int)(threadIdx.x & 15), w = (int)blockIdx.y;
+  const int n = (int)(threadIdx.x & 15);
   const KvRow row = locate(a, r);
-  if (row.cache < 0) return;
-  const T* src = reinterpret_cast<const T*>(a.rows[w]) + row.t * a.stride_t[w] + row.h * a.stride_h[w] + 2 * n;
-  float x[NB][2];
+  float x[2][NB][2];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) load_pair(src + 32 * b, x[b]);
-  if constexpr (FMT == NVQ_KV_Q8_0) {
-    uint16_t code[NB], scale[NB];
+  for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const uint32_t u0 = __builtin_bit_cast(uint32_t, x[b][0]) & 0x7FFFFFFFu;
-      const uint32_t u1 = __builtin_bit_cast(uint32_t, x[b][1]) & 0x7FFFFFFFu;
-      // the activation quantiser's arithmetic: IEEE divisions, ties to even.  An infinite
-      // or NaN element makes the scale infinite or NaN and the codes 0: the block reads
-      // back as NaN, never as numbers.
-      const float d = __builtin_bit_cast(float, row16_umax(max(u0, u1))) / 127.0f;
-      int q0 = 0, q1 = 0;
-      if (d > 0.0f && d < __builtin_inff()) {
-        q0 = (int)fminf(fmaxf(__builtin_rintf(x[b][0] / d), -127.0f), 127.0f);
-        q1 = (int)fminf(fmaxf(__builtin_rintf(x[b][1] / d), -127.0f), 127.0f);
+    for (int b = 0; b < NB; ++b) load_pair(row_at<T>(a, row, w) + 32 * b, x[w][b]);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    if constexpr (FMT == NVQ_KV_Q8_0) {
+      uint16_t code[NB], scale[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const uint32_t u0 = __builtin_bit_cast(uint32_t, x[w][b][0]) & 0x7FFFFFFFu;
+        const uint32_t u1 = __builtin_bit_cast(uint32_t, x[w][b][1]) & 0x7FFFFFFFu;
+        code[b] = quant_pair(x[w][b], row16_umax(max(u0, u1)), scale[b]);
       }
-      code[b] = (uint16_t)((q0 & 0xFF) | ((q1 & 0xFF) << 8));
-      scale[b] = __builtin_bit_cast(uint16_t, (_Float16)d);
-    }
-    store_halves<NB>(a.codes[w] + row.cache * (32 * NB) + 2 * NB * n, code);
-    if (n == 0) store_halves<NB>(a.scales[w] + row.cache * NB, scale);
-  } else {
-    // one rounding, to nearest even, to the cache's type
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.codes[w] + row.cache * (64 * NB)) + n;
+      if (row.cache >= 0) {
+        store_halves<NB>(a.codes[w] + row.cache * (32 * NB) + 2 * NB * n, code);
+        if (n == 0) store_halves<NB>(a.scales[w] + row.cache * NB, scale);
+      }
+    } else if (row.cache >= 0) {
+      // one rounding, to nearest even, to the cache's type
+      uint32_t* dst = reinterpret_cast<uint32_t*>(a.codes[w] + row.cache * (64 * NB)) + n;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) dst[16 * b] = pack_pair<typename CacheType<FMT>::type>(x[b][0], x[b][1]);
+      for (int b = 0; b < NB; ++b) dst[16 * b] = pack_pair<typename CacheType<FMT>::type>(x[w][b][0], x[w][b][1]);
+    }
   }
 }
 
 template <typename T, int FMT, int NB>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a) {
-  const int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int r = (int)blockIdx.x * 16 + (int)(threadIdx.x >> 4);
   if (r >= a.n_rows) return;
-  const int n = (int)(threadIdx.x & 15), w = (int)blockIdx.y;
+  const int n = (int)(threadIdx.x & 15);
   const KvRow row = locate(a, r);
-  T* dst = reinterpret_cast<T*>(const_cast<void*>(a.rows[w])) + row.t * a.stride_t[w] + row.h * a.stride_h[w] + 2 * n;
-  float x[NB][2];
-  if (row.cache < 0) {
-    const float v = row.cache == -1 ? 0.0f : __builtin_nanf("");
+  const int64_t at = max(row.cache, (int64_t)0);  // a slot that names no row: any row, unused
+  float x[2][NB][2];
+  if constexpr (FMT == NVQ_KV_Q8_0) {
+    uint16_t code[2][NB], scale[2][NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) x[b][0] = x[b][1] = v;
-  } else if constexpr (FMT == NVQ_KV_Q8_0) {
-    uint16_t code[NB], scale[NB];
-    load_halves<NB>(a.codes[w] + row.cache * (32 * NB) + 2 * NB * n, code);
-    load_halves<NB>(a.scales[w] + row.cache * NB, scale);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const float d = f16_bits_to_f32(scale[b]);
-      x[b][0] = (float)(int8_t)(code[b] & 0xFF) * d;  // 8 + 11 significant bits: exact
-      x[b][1] = (float)(int8_t)(code[b] >> 8) * d;
+    for (int w = 0; w < 2; ++w) {
+      load_halves<NB>(a.codes[w] + at * (32 * NB) + 2 * NB * n, code[w]);
+      load_halves<NB>(a.scales[w] + at * NB, scale[w]);
     }
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float d = f16_bits_to_f32(scale[w][b]);
+        x[w][b][0] = (float)(int8_t)(code[w][b] & 0xFF) * d;  // 8 + 11 significant bits: exact
+        x[w][b][1] = (float)(int8_t)(code[w][b] >> 8) * d;
+      }
   } else {
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(a.codes[w] + row.cache * (64 * NB)) + n;
+    uint32_t pair[2][NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) unpack_pair<typename CacheType<FMT>::type>(src[16 * b], x[b]);
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) pair[w][b] = reinterpret_cast<const uint32_t*>(a.codes[w] + at * (64 * NB))[16 * b + n];
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) unpack_pair<typename CacheType<FMT>::type>(pair[w][b], x[w][b]);
   }
+  const float none = row.cache == -1 ? 0.0f : __builtin_nanf("");
 #pragma unroll
-  for (int b = 0; b < NB; ++b) store_pair(dst + 32 * b, x[b][0], x[b][1]);
+  for (int w = 0; w < 2; ++w) {
+    T* dst = const_cast<T*>(row_at<T>(a, row, w));
+#pragma unroll
+    for (int b = 0; b < NB; ++b) store_pair(dst + 32 * b, row.cache < 0 ? none : x[w][b][0], row.cache < 0 ? none : x[w][b][1]);
+  }
 }
 
 template <typename T, int FMT, int NB>
 void launch_nb(const KvArgs& a, bool write, hipStream_t s) {
-  const dim3 grid((unsigned)((a.n_rows + 15) / 16), 2);
+  const dim3 grid(((unsigned)a.n_rows + 15) / 16);
   if (write)
     hipLaunchKernelGGL((kv_write_kernel<T, FMT, NB>), grid, dim3(256), 0, s, a);
   else
@@ -212,7 +246,7 @@ hipError_t launch_kv_copy(bool write, int fmt, int type, const void* k, const vo
   a.codes[0] = (uint8_t*)c.k, a.codes[1] = (uint8_t*)c.v;
   a.scales[0] = (uint16_t*)c.k_d, a.scales[1] = (uint16_t*)c.v_d;
   a.slots = slots;
-  a.n_rows = T * heads;
+  a.n_rows = (int)(T * heads);
   a.n_slots = c.n_pages << c.page_shift;
   a.heads = (uint32_t)heads;
   a.page_shift = (uint32_t)c.page_shift;

@@ -681,7 +681,7 @@ nvq_status kv_copy(bool write, const char* who, int fmt, int type, const void* k
   if (type < NVQ_TYPE_F32 || type > NVQ_TYPE_BF16) return fail(NVQ_ERR_RANGE, "%s: type=%d is not NVQ_TYPE_*", who, type);
   nvq::KvCache c;
   NVQ_TRY(check_cache(who, fmt, k_cache, v_cache, k_d, v_d, Hkv, D, n_pages, page, c));
-  if (T < 0 || T >= (int64_t(1) << 34) / Hkv) return fail(NVQ_ERR_SHAPE, "%s: T=%lld out of range", who, (long long)T);
+  if (T < 0 || T > ((int64_t(1) << 31) - 16) / Hkv) return fail(NVQ_ERR_SHAPE, "%s: T=%lld out of range", who, (long long)T);
   if (T == 0) return NVQ_OK;
   if (!k || !v || !slots) return fail(NVQ_ERR_NULL, "%s: NULL pointer", who);
   NVQ_TRY(check_rows(who, "k", k, type, T, Hkv, k_st, k_sh));
@@ -767,6 +767,9 @@ nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v
   NVQ_TRY(check_rows(who, "v", v, type, Tk, Hkv, strides[4], strides[5]));
   NVQ_TRY(check_rows(who, "out", out, type, Tq, Hq, strides[6], strides[7]));
   NVQ_TRY(check_apart(who, "out", Tq, Hq, D, strides[6], strides[7]));
+  // a tile's 64 rows are addressed by 32-bit offsets
+  if (Tk > 1 && (strides[2] >= (int64_t(1) << 24) || strides[4] >= (int64_t(1) << 24)))
+    return fail(NVQ_ERR_SHAPE, "%s: token strides of k and v must be below 2^24 elements", who);
   if (!aligned(cu_q, 4) || !aligned(cu_k, 4)) return fail(NVQ_ERR_ALIGN, "%s: cu_q and cu_k must be 4-byte aligned", who);
   if (nvq::attn_prompt_groups(B, Tq, Hq) >= kMaxDim) return fail(NVQ_ERR_SHAPE, "%s: too many query tiles", who);
   NVQ_TRY(check_device());

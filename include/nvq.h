@@ -475,7 +475,7 @@ nvq_status nvq_gemm_iq4_xs(const void* w, const int8_t* table, const int8_t* q, 
  * otherwise.  T = 0 or B = 0 is NVQ_OK and enqueues nothing. */
 
 /* Rows of T tokens into the cache: k, v [T][Hkv][D] of `type` (strides between tokens and
- * between heads), token t to slot slots[t] (device, int64).  A negative slot, or one past
+ * between heads; T * Hkv below 2^31), token t to slot slots[t] (device, int64).  A negative slot, or one past
  * the cache, writes nothing.  A slot given twice in one call gets one of the two rows,
  * or parts of both.  Q8_0: codes and scales are those of nvq_quantize_act_q8_0 on the row
  * as float32; a 32-channel block with an infinity or NaN reads back as NaN.  16-bit
@@ -519,7 +519,7 @@ nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b,
  * keys, query i sees keys j <= i + n - m if causal (the last query sees all: n > m puts the
  * queries behind n - m keys of a prefix), else all n.  A query that sees no key gives zeros.
  * `type` NVQ_TYPE_F16 or BF16; strides[8]: token and head stride of q, k, v and out (host).
- * Hq a multiple of Hkv; Tq, Tk < 2^30.  Rows of out in no sequence are left alone; offsets
+ * Hq a multiple of Hkv; Tq, Tk < 2^30; token strides of k and v below 2^24 elements.  Rows of out in no sequence are left alone; offsets
  * outside the tensors are cut to them.  Scores, softmax statistics and accumulation are
  * float32; the probabilities enter the second product rounded once to `type`. */
 nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v, void* out,

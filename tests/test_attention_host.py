@@ -69,7 +69,8 @@ def test_decode_refusals(want, kw):
     (SHAPE, dict(Hkv=0)), (SHAPE, dict(B=-1)), (SHAPE, dict(Tq=-1)), (SHAPE, dict(Tk=1 << 30)), (ALIGN, dict(q=P + 2)), (ALIGN, dict(out=P + 8)),
     (ALIGN, dict(cu_q=P + 2)), (ALIGN, dict(strides=(5124, 128, 1024, 128, 1024, 128, 5120, 128))),
     (SHAPE, dict(strides=(5120, 128, 1024, 128, 1024, 128, 0, 128))), (SHAPE, dict(strides=(5120, 128, 1024, 128, 1024, 128, 5120, 64))),
-    (SHAPE, dict(strides=(5120, -128, 1024, 128, 1024, 128, 5120, 128)))])
+    (SHAPE, dict(strides=(5120, -128, 1024, 128, 1024, 128, 5120, 128))), (SHAPE, dict(strides=(5120, 128, 1 << 24, 128, 1024, 128, 5120, 128))),
+    (SHAPE, dict(strides=(5120, 128, 1024, 128, 1 << 25, 128, 5120, 128)))])
 def test_prompt_refusals(want, kw):
     assert prompt(**kw) == want
     assert "nvq_attn_prompt" in nvq.last_error()
