@@ -11,6 +11,7 @@ every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -719,6 +720,7 @@ def nvq_kv_read(k_cache, v_cache, slots, k, v, k_d=None, v_d=None, stream=None) 
     _kv_copy(L.nvq_kv_read, "nvq_kv_read", k, v, slots, k_cache, v_cache, k_d, v_d, stream)
 
 
+@functools.lru_cache(maxsize=256)  # a function of its arguments alone; a decode loop asks it each step
 def nvq_attn_decode_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, max_pages: int, page: int) -> int:
     return int(lib().nvq_attn_decode_workspace_bytes(B, Hq, Hkv, D, max_pages, page))
 
@@ -738,7 +740,7 @@ def nvq_attn_decode(q, k_cache, v_cache, table, lengths, out, k_d=None, v_d=None
     tp, lp = _dense(table, _torch.int32, (B, max_pages), "table"), _dense(lengths, _torch.int32, (B,), "lengths")
     on = _on_device(stream, q, k_cache, v_cache, table, lengths, out, k_d, v_d, workspace)
     if workspace is None:
-        workspace = _workspace(L.nvq_attn_decode_workspace_bytes(B, Hq, heads, D, max_pages, page), stream, q)
+        workspace = _workspace(nvq_attn_decode_workspace_bytes(B, Hq, heads, D, max_pages, page), stream, q)
     wp, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
     st = L.nvq_attn_decode(fmt, _row_types[dtype], q.data_ptr(), qs[0], qs[1], B, Hq, heads, D, kp, vp, kdp, vdp, n_pages, page, tp, max_pages, lp,
                            D ** -0.5 if scale is None else scale, op, wp, ws_bytes, on)

@@ -62,12 +62,6 @@ struct Plan {
   bool bad;
 };
 
-__device__ __forceinline__ int wave_sum(int v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-
 // want_b: find sequence `want`, else find the sequence of chunk `want`.  The whole wavefront
 // calls it; the answer is uniform.  Capacities are below 2^31 keys in all (host check).
 __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int want, bool want_b) {
@@ -78,7 +72,7 @@ __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int want, bool wa
     const int n = a.lengths[i];
     total += n < 0 || n > cap ? 0 : n;
   }
-  total = __builtin_amdgcn_readfirstlane(wave_sum(total));
+  total = __builtin_amdgcn_readlane(wave_running_sum(total), 63);
   Plan p;
   // chunk >= total / target, so there are at most target + B chunks (chunk_bound); a multiple of
   // a step of four wavefronts
@@ -95,12 +89,7 @@ __device__ __forceinline__ Plan make_plan(const DecodeArgs& a, int want, bool wa
     const bool bad = raw < 0 || raw > cap;
     const int n = bad ? 0 : raw;
     const int chunks = i < a.B ? max(1, (int)(((uint32_t)n + (uint32_t)p.chunk - 1) / (uint32_t)p.chunk)) : 0;
-    int incl = chunks;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int t = __shfl_up(incl, o, 64);
-      incl += lane >= o ? t : 0;
-    }
+    const int incl = wave_running_sum(chunks);
     const uint64_t hit = __ballot(want_b ? i == want : base + incl > want);
     if (hit) {
       const int l = __builtin_ctzll(hit);

@@ -73,26 +73,22 @@ __device__ __forceinline__ bool find_span(const PromptArgs& a, int want, Span& s
   int base = 0;
   for (int i0 = 0; i0 < a.B; i0 += 64) {
     const int i = i0 + lane;
-    int lo = 0, hi = 0;
-    if (i < a.B) {
-      lo = min(max(a.cu_q[i], 0), a.Tq);
-      hi = min(max(a.cu_q[i + 1], lo), a.Tq);
+    int lo = 0, hi = 0, key_lo = 0, key_hi = 0;
+    if (i < a.B) {  // (both tensors' offsets in one round trip to memory)
+      lo = a.cu_q[i], hi = a.cu_q[i + 1], key_lo = a.cu_k[i], key_hi = a.cu_k[i + 1];
+      lo = min(max(lo, 0), a.Tq), hi = min(max(hi, lo), a.Tq);
+      key_lo = min(max(key_lo, 0), a.Tk), key_hi = min(max(key_hi, key_lo), a.Tk);
     }
     const int tiles = (hi - lo + kQueries - 1) / kQueries;
-    int incl = tiles;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int t = __shfl_up(incl, o, 64);
-      incl += lane >= o ? t : 0;
-    }
+    const int incl = wave_running_sum(tiles);
     const uint64_t hit = __ballot(base + incl > want);
     if (hit) {
       const int l = __builtin_ctzll(hit);
       s.q0 = __builtin_amdgcn_readlane(lo, l);
       s.m = __builtin_amdgcn_readlane(hi, l) - s.q0;
       s.tile = base + __builtin_amdgcn_readlane(incl, l) - 1 - want;
-      s.k0 = min(max(a.cu_k[i0 + l], 0), a.Tk);
-      s.n = min(max(a.cu_k[i0 + l + 1], s.k0), a.Tk) - s.k0;
+      s.k0 = __builtin_amdgcn_readlane(key_lo, l);
+      s.n = __builtin_amdgcn_readlane(key_hi, l) - s.k0;
       return true;
     }
     base += __builtin_amdgcn_readlane(incl, 63);
@@ -142,17 +138,6 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
   // from here on a tile has keys that some of the wavefront's queries do not see
   const int whole = (a.causal ? min(sp.n, max(iw + shift + 1, 0)) : sp.n) / kKeys;
 
-  Frag qf[2 * NB];
-  {
-    const uint16_t* row = a.q + (int64_t)(sp.q0 + min(i, sp.m - 1)) * a.q_t + (int64_t)head * a.q_h;
-#pragma unroll
-    for (int ks = 0; ks < 2 * NB; ++ks) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(row + 16 * ks + 8 * hi);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) qf[ks].v[j] = w[j] ^ a.flip;
-    }
-  }
-
   // Tiles on their way into LDS: load j of the wavefront takes 64 pieces, one a lane, in LDS
   // order.  A tile's descriptor ends behind the sequence's last row: what a load asks for past
   // it comes as zeros (and nothing is read), the same for whole tiles past the end.
@@ -171,6 +156,33 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
                      rows > 0 ? (uint32_t)(rows - 1) * (uint32_t)(2 * stride_t) + S::ROW : 0u);
   };
 
+  const auto load_values = [&](int t, int slot) __attribute__((always_inline)) {
+    const u32x4 values = tile_of(a.v, a.v_t, a.v_h, t);
+#pragma unroll
+    for (int j = 0; j < S::LOADS; ++j) buffer_to_lds(values, value_from[j], values_at + slot * S::BYTES + 1024 * j);
+  };
+  const auto load_keys = [&](int t, int slot) __attribute__((always_inline)) {
+    const u32x4 keys = tile_of(a.k, a.k_t, a.k_h, t);
+#pragma unroll
+    for (int j = 0; j < S::LOADS; ++j) buffer_to_lds(keys, key_from[j], keys_at + slot * S::BYTES + 1024 * j);
+  };
+  // (in the order in which they are needed: the queries come back behind the first tile)
+  if (tiles > 0) {
+    load_keys(0, 0);
+    load_values(0, 0);
+    load_keys(1, 1);
+  }
+  Frag qf[2 * NB];
+  {
+    const uint16_t* row = a.q + (int64_t)(sp.q0 + min(i, sp.m - 1)) * a.q_t + (int64_t)head * a.q_h;
+#pragma unroll
+    for (int ks = 0; ks < 2 * NB; ++ks) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(row + 16 * ks + 8 * hi);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) qf[ks].v[j] = w[j] ^ a.flip;
+    }
+  }
+
   floatx16 acc[NB];
 #pragma unroll
   for (int t = 0; t < NB; ++t)
@@ -188,20 +200,21 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
       value_offset[d] = in_vgpr((uint32_t)(row_in * S::ROW + 16 * S::value_piece(row_in, 4 * d + 2 * half + ((jj & 3) >> 1)) + 8 * (jj & 1)));
   }
   // S^T of the tile in a slot; between the products, the loads of the values and keys that
-  // come next (one behind every second product, so that none waits for the others' issue)
+  // come next, one to two products, so that none waits for the others' issue
   const auto scores = [&](int slot, floatx16 (&s)[2], auto load) __attribute__((always_inline)) {
     const uint8_t* tile = s_keys + slot * S::BYTES;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int j = 0; j < 16; ++j) s[kb][j] = 0.0f;
 #pragma unroll
-      for (int ks = 0; ks < 2 * NB; ++ks) {
+    for (int ks = 0; ks < 2 * NB; ++ks)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
         const u32x4 w = *reinterpret_cast<const u32x4*>(tile + key_offset[ks] + 32 * kb * S::ROW);
         s[kb] = mfma32<T>(Frag{w[0], w[1], w[2], w[3]}, qf[ks], s[kb]);
-        if (ks % 2) load(kb * NB + ks / 2);
+        if (kb) load(ks);
       }
-    }
   };
   // Tile t: no score for keys that the query does not see; then its largest (the lane's part)
   const auto largest = [&](floatx16 (&s)[2]) __attribute__((always_inline)) {
@@ -280,21 +293,8 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  const auto load_values = [&](int t, int slot) __attribute__((always_inline)) {
-    const u32x4 values = tile_of(a.v, a.v_t, a.v_h, t);
-#pragma unroll
-    for (int j = 0; j < S::LOADS; ++j) buffer_to_lds(values, value_from[j], values_at + slot * S::BYTES + 1024 * j);
-  };
-  const auto load_keys = [&](int t, int slot) __attribute__((always_inline)) {
-    const u32x4 keys = tile_of(a.k, a.k_t, a.k_h, t);
-#pragma unroll
-    for (int j = 0; j < S::LOADS; ++j) buffer_to_lds(keys, key_from[j], keys_at + slot * S::BYTES + 1024 * j);
-  };
   floatx16 sa[2], sb[2];
   if (tiles > 0) {
-    load_keys(0, 0);
-    load_values(0, 0);
-    load_keys(1, 1);
     turn();
     if (mine > 0) {
       scores(0, sa, [](int) __attribute__((always_inline)) {});
