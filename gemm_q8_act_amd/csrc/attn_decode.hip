@@ -146,6 +146,9 @@ struct Shape {
   static constexpr int SLOT = 4 * GROUP + 4 * SCALES;
   // Two tiles' room a wavefront.  Rows wider than 256 bytes leave room for two wavefronts.
   static constexpr int WAVES = 2 * 4 * SLOT <= 144 * 1024 ? 4 : 2;
+  // Wavefronts of a SIMD that the registers are cut for: two, so that the accumulator stays in
+  // ordinary registers (with one it moves to the other half and back in every step), where it all fits.
+  static constexpr int EU_WAVES = NB <= (Q8 ? 4 : 5) ? 2 : 1;
   // 16-byte pieces of a key row, and which row bits they are exchanged by in LDS, so that the
   // lanes of one piece of different rows fall on different banks (64 of 4 bytes)
   static constexpr int PIECES = ROW / 16;
@@ -254,9 +257,15 @@ __device__ __forceinline__ float split_queries(int type, const u32x4 (&raw)[NB][
   return back;
 }
 
-template <int FMT, int NB>
-__global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES)) void attn_decode_kernel(DecodeArgs a) {
+// Q (Q8_0): columns to a head.  With few query heads to a key head most of the 16 columns would
+// be idle while every lane multiplies its probabilities by all blocks' value scales and splits
+// them; so a head takes Q columns, and column q of them carries P times the scales of blocks q,
+// q + Q, .. only.  All columns go through the products; of a block's channels, the column that
+// carries its scale is the result.
+template <int FMT, int NB, int Q>
+__global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES), (Shape<FMT, NB>::EU_WAVES)) void attn_decode_kernel(DecodeArgs a) {
   typedef Shape<FMT, NB> S;
+  constexpr int SETS = (NB + Q - 1) / Q;  // blocks of a column
   constexpr int kWaves = S::WAVES;
   typedef typename CacheType<FMT>::type T;
   const int lane = (int)(threadIdx.x & 63), n = lane & 15, g = lane >> 4;
@@ -271,9 +280,10 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES)) void attn_decode_kern
 
   // The query heads' rows on their way, in the keys' operand order: block bl, slot (g, s) is
   // channel 32 bl + 8 g + s.  Columns past the last head read it again.
-  const bool live = h0 + n < a.G;
+  const int head = h0 + n / Q, group = n % Q;
+  const bool live = head < a.G;
   u32x4 q_raw[NB][2];
-  load_queries<NB>(a, b * a.q_stride_b + (int64_t)(kvh * a.G + min(h0 + n, a.G - 1)) * a.q_stride_h + 8 * g, q_raw);
+  load_queries<NB>(a, b * a.q_stride_b + (int64_t)(kvh * a.G + min(head, a.G - 1)) * a.q_stride_h + 8 * g, q_raw);
 
   floatx4 acc[S::TILES];
 #pragma unroll
@@ -354,7 +364,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES)) void attn_decode_kern
       wait_loads<S::V_LOADS + S::K_LOADS + S::V_LOADS>();
     else
       wait_loads<S::V_LOADS>();
-    uint32_t kw[2][S::KW], kd[2][S::DW], vd[2][S::DW];
+    uint32_t kw[2][S::KW], kd[2][S::DW];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const uint8_t* p = slot + u * S::GROUP + n * S::ROW;
@@ -368,9 +378,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES)) void attn_decode_kern
         for (int bl = 0; bl < NB; ++bl) read_dwords<4>(p + 16 * S::piece(n, 4 * bl + g), kw[u] + 4 * bl);
       }
       if constexpr (S::Q8) {
-        const uint8_t* d = slot + 4 * S::GROUP + u * S::SCALES + 8 * NB * g;
-        read_dwords<S::DW>(d, kd[u]);
-        read_dwords<S::DW>(d + 2 * S::SCALES, vd[u]);
+        read_dwords<S::DW>(slot + 4 * S::GROUP + u * S::SCALES + 8 * NB * g, kd[u]);
       }
     }
     const bool more = t + 2 < mine;
@@ -417,10 +425,16 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES)) void attn_decode_kern
     else
       wait_loads<0>();
     uint32_t vw[2][4][S::VW];
+    uint16_t vd[S::Q8 ? SETS : 1][8];  // the value scales that the column carries
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if constexpr (S::Q8) {
+          const uint16_t* d = reinterpret_cast<const uint16_t*>(slot + 4 * S::GROUP + (2 + u) * S::SCALES) + (4 * g + i) * NB;
+#pragma unroll
+          for (int t2 = 0; t2 < SETS; ++t2) vd[t2][4 * u + i] = d[min(t2 * Q + group, NB - 1)];
+        }
         const uint8_t* p = slot + (2 + u) * S::GROUP + (4 * g + i) * S::ROW;
         if constexpr (!S::Q8) {
           read_dwords<S::VW>(p + 4 * NB * n, vw[u][i]);
@@ -448,10 +462,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES)) void attn_decode_kern
             sc[4 * u + i] = -__builtin_inff();
             if constexpr (S::Q8) {
 #pragma unroll
-              for (int bl = 0; bl < NB; ++bl) {
-                const int at = i * NB + bl;
-                vd[u][at >> 1] &= at & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-              }
+              for (int t2 = 0; t2 < SETS; ++t2) vd[t2][4 * u + i] = 0;
             } else {
 #pragma unroll
               for (int w = 0; w < S::VW; ++w) vw[u][i][w] = 0;
@@ -482,21 +493,20 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES)) void attn_decode_kern
     }
     if constexpr (S::Q8) {
 #pragma unroll
-      for (int bl = 0; bl < NB; ++bl) {
+      for (int t2 = 0; t2 < SETS; ++t2) {
         float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(half_of(vd[i >> 2], (i & 3) * NB + bl), p[i], 0.0f);
+        for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(f16_bits_to_f32(vd[t2][i]), p[i], 0.0f);
         Frag pf[S::P_TERMS];
         split_terms<typename S::P, S::P_TERMS>(x, pf);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {  // channels 32 bl + 2 n + e
+        for (int at = 2 * Q * t2; at < 2 * min(Q * t2 + Q, NB); ++at) {  // channels 32 (at / 2) + 2 n + at % 2
           Frag f;
-          const int at = 2 * bl + e;
 #pragma unroll
           for (int j = 0; j < 4; ++j)  // keys 2 j, 2 j + 1 of the lane's eight
             f.v[j] = codes_to_bf16(vw[j >> 1][2 * (j & 1)][at >> 2], vw[j >> 1][2 * (j & 1) + 1][at >> 2], at & 3);
 #pragma unroll
-          for (int k = 0; k < S::P_TERMS; ++k) acc[2 * bl + e] = mfma16<typename S::P>(f, pf[k], acc[2 * bl + e]);
+          for (int k = 0; k < S::P_TERMS; ++k) acc[at] = mfma16<typename S::P>(f, pf[k], acc[at]);
         }
       }
     } else {
@@ -555,10 +565,11 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES)) void attn_decode_kern
   if (!live) return;
   // no key, or none with a probability: zeros
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int64_t at = ((int64_t)b * a.Hq + kvh * a.G + h0 + n) * (32 * NB);
+  const int64_t at = ((int64_t)b * a.Hq + kvh * a.G + head) * (32 * NB);
   if constexpr (S::Q8) {
 #pragma unroll
     for (int bl = 0; bl < NB; ++bl) {
+      if (group != bl % Q) continue;
       float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = acc[2 * bl + (i & 1)][i >> 1] * inv;
@@ -579,7 +590,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES)) void attn_decode_kern
 // wavefronts, APART take 16-channel tiles of their own and the others share those tiles'
 // chunks: all eight apart where there are sequences enough to fill the chip (64 sequences of
 // about 4 chunks, 128 channels: 5 us; sharing 15), none where a few sequences have many chunks.
-template <int FMT, int NB, int APART>
+template <int FMT, int NB, int Q, int APART>
 __global__ __launch_bounds__(64 * kJoinWaves) void attn_decode_join_kernel(DecodeArgs a) {
   typedef Shape<FMT, NB> S;
   constexpr int kWaves = kJoinWaves / APART;
@@ -641,10 +652,10 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_decode_join_kernel(Decod
     for (int w = 0; w < kWaves - 1; ++w) acc += s_acc[w][lane], sum += s_sum[w][lane];
   }
   if (!in) return;
-  const int kvh = hh / a.HT, h0 = (hh - kvh * a.HT) * 16;
-  if (h0 + n >= a.G) return;
+  const int kvh = hh / a.HT, head = (hh - kvh * a.HT) * 16 + n / Q;
+  if (head >= a.G || n % Q != (tile >> 1) % Q) return;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int64_t at = ((int64_t)b * a.Hq + kvh * a.G + h0 + n) * (32 * NB);
+  const int64_t at = ((int64_t)b * a.Hq + kvh * a.G + head) * (32 * NB);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int ch = S::Q8 ? 32 * (tile >> 1) + 8 * g + 2 * i + (tile & 1) : 2 * NB * (4 * g + i) + tile;
@@ -665,17 +676,32 @@ int64_t chunk_bound(int64_t B, int64_t Hkv, int64_t G, int64_t capacity) {
   return most < t ? most : t;
 }
 
-template <int FMT, int NB>
-hipError_t launch_nb(const DecodeArgs& a, int64_t blocks, bool join, hipStream_t s) {
-  hipLaunchKernelGGL((attn_decode_kernel<FMT, NB>), dim3((unsigned)blocks), dim3(64 * Shape<FMT, NB>::WAVES), 0, s, a);
+template <int FMT, int NB, int Q>
+hipError_t launch_q(const DecodeArgs& a, int64_t blocks, bool join, hipStream_t s) {
+  hipLaunchKernelGGL((attn_decode_kernel<FMT, NB, Q>), dim3((unsigned)blocks), dim3(64 * Shape<FMT, NB>::WAVES), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !join) return e;
   const unsigned rows = (unsigned)(a.B * a.Hkv * a.HT);
   if (rows >= 256)
-    hipLaunchKernelGGL((attn_decode_join_kernel<FMT, NB, kJoinWaves>), dim3(rows, (2 * NB + kJoinWaves - 1) / kJoinWaves), dim3(64 * kJoinWaves), 0, s, a);
+    hipLaunchKernelGGL((attn_decode_join_kernel<FMT, NB, Q, kJoinWaves>), dim3(rows, (2 * NB + kJoinWaves - 1) / kJoinWaves), dim3(64 * kJoinWaves), 0, s, a);
   else
-    hipLaunchKernelGGL((attn_decode_join_kernel<FMT, NB, 1>), dim3(rows, 2 * NB), dim3(64 * kJoinWaves), 0, s, a);
+    hipLaunchKernelGGL((attn_decode_join_kernel<FMT, NB, Q, 1>), dim3(rows, 2 * NB), dim3(64 * kJoinWaves), 0, s, a);
   return hipGetLastError();
+}
+template <int FMT, int NB>
+hipError_t launch_nb(const DecodeArgs& a, int64_t blocks, bool join, hipStream_t s) {
+  if constexpr (FMT == NVQ_KV_Q8_0) {
+    if constexpr (NB >= 4) {
+      if (a.G <= 4) return launch_q<FMT, NB, 4>(a, blocks, join, s);
+    }
+    if constexpr (NB >= 3) {
+      if (a.G <= 5) return launch_q<FMT, NB, 3>(a, blocks, join, s);
+    }
+    if constexpr (NB >= 2) {
+      if (a.G <= 8) return launch_q<FMT, NB, 2>(a, blocks, join, s);
+    }
+  }
+  return launch_q<FMT, NB, 1>(a, blocks, join, s);
 }
 template <int FMT>
 hipError_t launch_fmt(const DecodeArgs& a, int nb, int64_t blocks, bool join, hipStream_t s) {
