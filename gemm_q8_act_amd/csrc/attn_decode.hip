@@ -365,6 +365,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES), (Shape<FMT, NB>::EU_W
     else
       wait_loads<S::V_LOADS>();
     uint32_t kw[2][S::KW], kd[2][S::DW];
+    uint16_t vd[S::Q8 ? SETS : 1][8];  // the value scales that the column carries
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const uint8_t* p = slot + u * S::GROUP + n * S::ROW;
@@ -378,7 +379,14 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES), (Shape<FMT, NB>::EU_W
         for (int bl = 0; bl < NB; ++bl) read_dwords<4>(p + 16 * S::piece(n, 4 * bl + g), kw[u] + 4 * bl);
       }
       if constexpr (S::Q8) {
+        // both tensors' scales come and go with the keys: they are read before the next keys are
+        // sent for
         read_dwords<S::DW>(slot + 4 * S::GROUP + u * S::SCALES + 8 * NB * g, kd[u]);
+        const uint16_t* d = reinterpret_cast<const uint16_t*>(slot + 4 * S::GROUP + (2 + u) * S::SCALES) + 4 * g * NB;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int set = 0; set < SETS; ++set) vd[set][4 * u + i] = d[i * NB + min(set * Q + group, NB - 1)];
       }
     }
     const bool more = t + 2 < mine;
@@ -425,16 +433,10 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES), (Shape<FMT, NB>::EU_W
     else
       wait_loads<0>();
     uint32_t vw[2][4][S::VW];
-    uint16_t vd[S::Q8 ? SETS : 1][8];  // the value scales that the column carries
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if constexpr (S::Q8) {
-          const uint16_t* d = reinterpret_cast<const uint16_t*>(slot + 4 * S::GROUP + (2 + u) * S::SCALES) + (4 * g + i) * NB;
-#pragma unroll
-          for (int t2 = 0; t2 < SETS; ++t2) vd[t2][4 * u + i] = d[min(t2 * Q + group, NB - 1)];
-        }
         const uint8_t* p = slot + (2 + u) * S::GROUP + (4 * g + i) * S::ROW;
         if constexpr (!S::Q8) {
           read_dwords<S::VW>(p + 4 * NB * n, vw[u][i]);
@@ -462,7 +464,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES), (Shape<FMT, NB>::EU_W
             sc[4 * u + i] = -__builtin_inff();
             if constexpr (S::Q8) {
 #pragma unroll
-              for (int t2 = 0; t2 < SETS; ++t2) vd[t2][4 * u + i] = 0;
+              for (int set = 0; set < SETS; ++set) vd[set][4 * u + i] = 0;
             } else {
 #pragma unroll
               for (int w = 0; w < S::VW; ++w) vw[u][i][w] = 0;
@@ -493,14 +495,14 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES), (Shape<FMT, NB>::EU_W
     }
     if constexpr (S::Q8) {
 #pragma unroll
-      for (int t2 = 0; t2 < SETS; ++t2) {
+      for (int set = 0; set < SETS; ++set) {
         float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(f16_bits_to_f32(vd[t2][i]), p[i], 0.0f);
+        for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(f16_bits_to_f32(vd[set][i]), p[i], 0.0f);
         Frag pf[S::P_TERMS];
         split_terms<typename S::P, S::P_TERMS>(x, pf);
 #pragma unroll
-        for (int at = 2 * Q * t2; at < 2 * min(Q * t2 + Q, NB); ++at) {  // channels 32 (at / 2) + 2 n + at % 2
+        for (int at = 2 * Q * set; at < 2 * min(Q * set + Q, NB); ++at) {  // channels 32 (at / 2) + 2 n + at % 2
           Frag f;
 #pragma unroll
           for (int j = 0; j < 4; ++j)  // keys 2 j, 2 j + 1 of the lane's eight

@@ -60,6 +60,14 @@ def test_lengths_that_are_split(fmt, lens, page):
     run(fmt, "f32", lens, 5, 1, 128, page, sum(lens))
 
 
+@pytest.mark.parametrize("fmt", ["q8_0", "f16", "bf16"])
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page", [([20011, 900], 16, 16, 64, 64), ([21500], 80, 16, 128, 256), ([5000, 0, 3900], 128, 64, 32, 16),
+                                                ([4100], 64, 32, 256, 16), ([9000, 31], 64, 32, 96, 32)])
+def test_parts_of_many_tiles(fmt, lens, Hq, Hkv, D, page):
+    """Many key heads, so that the parts are long: every wavefront takes 3 to 12 tiles in turn, over both slots."""
+    run(fmt, "f32", lens, Hq, Hkv, D, page, sum(lens) + D)
+
+
 def test_many_sequences():
     """More sequences than a wavefront has lanes, most of them short or empty."""
     r = np.random.Generator(np.random.PCG64(3))
