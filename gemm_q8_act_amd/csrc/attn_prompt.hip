@@ -104,16 +104,12 @@ template <int NB>
 struct Stage {
   static constexpr int ROW = 64 * NB, PIECES = 4 * NB, BYTES = kKeys * ROW;
   static constexpr int LOADS = BYTES / 1024 / kWaves;  // 1 KB loads of a wavefront
+  // (an exchange stays inside aligned groups of 16, 8 or 4 pieces, so it fits any row)
   static __device__ __forceinline__ int key_piece(int row, int i) {
-    if constexpr (PIECES == 16 || PIECES == 32) return i ^ (row & 15);
-    if constexpr (PIECES == 8) return i ^ ((row >> 1) & 7);
-    if constexpr (PIECES == 4) return i ^ ((row >> 2) & 3);
-    return i;
+    return PIECES % 16 == 0 ? i ^ (row & 15) : PIECES % 8 == 0 ? i ^ ((row >> 1) & 7) : i ^ ((row >> 2) & 3);
   }
   static __device__ __forceinline__ int value_piece(int row, int i) {
-    if constexpr (PIECES == 16 || PIECES == 32) return i ^ ((row & 3) << 2);
-    if constexpr (PIECES == 8) return i ^ ((row & 2) << 1);
-    return i;
+    return PIECES % 16 == 0 ? i ^ ((row & 3) << 2) : PIECES % 8 == 0 ? i ^ ((row & 2) << 1) : i;
   }
 };
 
