@@ -624,8 +624,9 @@ def nvq_debug_isums(fmt: int, path: int, w, q, N: int, isums, stream=None) -> No
 # paged key-value cache and attention
 # ---------------------------------------------------------------------------
 
-# A decode step makes these calls with a few microseconds of work each, so the checks below
-# compare types and shapes directly and say more only once something is wrong.
+# A decode step makes these calls with a few microseconds of work each.  Each one first asks
+# everything it needs to know of its tensors in one expression; only if something is wrong does
+# a second look (_wrong_*) find out what, and raise.
 _torch = None            # set with the tables
 _row_types: dict = {}    # torch dtype -> NVQ_TYPE_*
 _cache_types: dict = {}  # torch dtype -> NVQ_KV_*
@@ -641,67 +642,79 @@ def _attn_lib():
     return lib()
 
 
-def _rows(t, dtype, shape, name):
-    """A row tensor [rows, heads, D] whose channels are contiguous (its other strides are passed on): its strides."""
-    if t is None or t.dtype is not dtype or t.shape != shape:
-        _need(t, dtype, shape, name)
-    st = t.stride()
-    if st[2] != 1 and shape[2] > 1:
-        raise ValueError(f"{name}: a row's channels must be contiguous")
-    return st
-
-
-def _dense(t, dtype, shape, name):
-    if t is None or t.dtype is not dtype or t.shape != shape:
-        _need(t, dtype, shape, name)
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: tensors passed to libnvq must be contiguous")
-    return t.data_ptr()
-
-
-def _row_shape(t, name):
+def _wrong_rows(t, dtype, shape, name):
     if t is None or t.dim() != 3 or t.dtype not in _row_types:
         raise ValueError(f"{name}: a float32, float16 or bfloat16 tensor [rows, heads, D] is required")
-    return t.shape
+    _need(t, dtype, shape, name)
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}: a row's channels must be contiguous")
 
 
-def _on_device(stream, *tensors):
-    """Every tensor on the current GPU (pointers of another one must not reach a launch on this one's stream): the
-    stream to launch on."""
+def _wrong_dense(t, dtype, shape, name):
+    _need(t, dtype, shape, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors passed to libnvq must be contiguous")
+
+
+def _wrong_cache(k_cache, v_cache, k_d, v_d):
+    if k_cache is None or k_cache.dim() != 4 or k_cache.dtype not in _cache_types:
+        raise ValueError("k_cache: an int8 (Q8_0), float16 or bfloat16 tensor [n_pages, heads, page, D] is required")
+    _wrong_dense(k_cache, k_cache.dtype, k_cache.shape, "k_cache")
+    _wrong_dense(v_cache, k_cache.dtype, k_cache.shape, "v_cache")
+    d_shape = (*k_cache.shape[:3], k_cache.shape[3] // 32)
+    for t, name in ((k_d, "k_d"), (v_d, "v_d")):
+        if k_cache.dtype != _torch.int8:
+            if t is not None:
+                raise ValueError(f"{name}: a 16-bit cache has no scales")
+        elif t is None or t.shape != d_shape or t.element_size() != 2 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 2-byte tensor [n_pages, heads, page, D/32]")
+
+
+def _wrong_device(*tensors):
+    """Pointers of another GPU must not reach a launch on the current one's stream."""
     here = _torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != here:
             raise ValueError(f"tensor on {t.device}, expected the current device cuda:{here}")
-    return _torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream)
 
 
-def _kv_cache(k_cache, v_cache, k_d, v_d):
-    """(format, shape, the four pointers) of a cache [n_pages, heads, page, D]."""
-    fmt = None if k_cache is None or k_cache.dim() != 4 else _cache_types.get(k_cache.dtype)
-    if fmt is None:
-        raise ValueError("k_cache: an int8 (Q8_0), float16 or bfloat16 tensor [n_pages, heads, page, D] is required")
-    shape = k_cache.shape
-    kp, vp = _dense(k_cache, k_cache.dtype, shape, "k_cache"), _dense(v_cache, k_cache.dtype, shape, "v_cache")
-    if fmt != NVQ_KV_Q8_0:
-        if k_d is not None or v_d is not None:
-            raise ValueError("k_d, v_d: a 16-bit cache has no scales")
-        return fmt, shape, kp, vp, None, None
-    d_shape = (*shape[:3], shape[3] // 32)
-    for t in (k_d, v_d):
-        if t is None or t.shape != d_shape or t.element_size() != 2 or not t.is_contiguous():
-            raise ValueError("k_d and v_d must be contiguous 2-byte tensors [n_pages, heads, page, D/32]")
-    return fmt, shape, kp, vp, k_d.data_ptr(), v_d.data_ptr()
+def _cache_fine(fmt, shape, k_cache, v_cache, k_d, v_d):
+    """Whether a cache [n_pages, heads, page, D] and its scales fit together (all contiguous)."""
+    if not (v_cache.dtype is k_cache.dtype and v_cache.shape == shape and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        return False
+    if fmt:
+        return k_d is None and v_d is None
+    d_shape = (shape[0], shape[1], shape[2], shape[3] // 32)
+    return (k_d.shape == d_shape and v_d.shape == d_shape and k_d.element_size() == 2 and v_d.element_size() == 2
+            and k_d.is_contiguous() and v_d.is_contiguous())
 
 
 def _kv_copy(fn, name, k, v, slots, k_cache, v_cache, k_d, v_d, stream):
-    fmt, (n_pages, heads, page, D), kp, vp, kdp, vdp = _kv_cache(k_cache, v_cache, k_d, v_d)
-    T = _row_shape(k, "k")[0]
-    dtype = k.dtype
-    ks, vs = _rows(k, dtype, (T, heads, D), "k"), _rows(v, dtype, (T, heads, D), "v")
-    sp = _dense(slots, _torch.int64, (T,), "slots")
-    on = _on_device(stream, k, v, slots, k_cache, v_cache, k_d, v_d)
-    st = fn(fmt, _row_types[dtype], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], sp, T, heads, D, kp, vp, kdp, vdp, n_pages,
-            page, on)
+    here = -1
+    try:
+        fmt, shape, rows, dtype = _cache_types[k_cache.dtype], k_cache.shape, k.shape, k.dtype
+        n_pages, heads, page, D = shape
+        T = rows[0]
+        ks, vs, code = k.stride(), v.stride(), _row_types[dtype]
+        fine = (_cache_fine(fmt, shape, k_cache, v_cache, k_d, v_d) and rows == (T, heads, D) and v.shape == rows and v.dtype is dtype
+                and ks[2] == 1 and vs[2] == 1 and slots.dtype is _torch.int64 and slots.shape == rows[:1] and slots.is_contiguous())
+        if fine:
+            here = _torch.cuda.current_device()
+            fine = (k.get_device() == here and v.get_device() == here and slots.get_device() == here and k_cache.get_device() == here
+                    and v_cache.get_device() == here and (fmt or k_d.get_device() == here and v_d.get_device() == here))
+    except (AttributeError, KeyError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _wrong_cache(k_cache, v_cache, k_d, v_d)
+        T, (_, heads, _, D) = k.shape[0] if k is not None and k.dim() == 3 else -1, k_cache.shape
+        _wrong_rows(k, k.dtype if k is not None else None, (T, heads, D), "k")
+        _wrong_rows(v, k.dtype, (T, heads, D), "v")
+        _wrong_dense(slots, _torch.int64, (T,), "slots")
+        _wrong_device(k, v, slots, k_cache, v_cache, k_d, v_d)
+        raise ValueError("k, v, slots and the cache do not fit together")
+    st = fn(fmt, code, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slots.data_ptr(), T, heads, D, k_cache.data_ptr(), v_cache.data_ptr(),
+            None if fmt else k_d.data_ptr(), None if fmt else v_d.data_ptr(), n_pages, page,
+            _torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream))
     if st:
         _check(st, name)
 
@@ -730,20 +743,40 @@ def nvq_attn_decode(q, k_cache, v_cache, table, lengths, out, k_d=None, v_d=None
     """One new token per sequence: q [B, Hq, D] (strides free), the paged cache, table int32 [B, max_pages] and
     lengths int32 [B] -> out [B, Hq, D] of q's type.  scale: 1 / sqrt(D) unless given."""
     L = _lib if _torch is not None else _attn_lib()
-    fmt, (n_pages, heads, page, D), kp, vp, kdp, vdp = _kv_cache(k_cache, v_cache, k_d, v_d)
-    B, Hq, _ = _row_shape(q, "q")
-    dtype, shape = q.dtype, (B, Hq, D)
-    qs, op = _rows(q, dtype, shape, "q"), _dense(out, dtype, shape, "out")
-    if table is None or table.dim() != 2:
-        raise ValueError("table: int32 [B, max_pages] is required")
-    max_pages = table.shape[1]
-    tp, lp = _dense(table, _torch.int32, (B, max_pages), "table"), _dense(lengths, _torch.int32, (B,), "lengths")
-    on = _on_device(stream, q, k_cache, v_cache, table, lengths, out, k_d, v_d, workspace)
+    here = -1
+    try:
+        fmt, shape, rows, dtype = _cache_types[k_cache.dtype], k_cache.shape, q.shape, q.dtype
+        n_pages, heads, page, D = shape
+        B, Hq, max_pages = rows[0], rows[1], table.shape[1]
+        qs, code, i32 = q.stride(), _row_types[dtype], _torch.int32
+        fine = (_cache_fine(fmt, shape, k_cache, v_cache, k_d, v_d) and rows == (B, Hq, D) and out.shape == rows and out.dtype is dtype
+                and qs[2] == 1 and out.is_contiguous() and table.dtype is i32 and table.shape == (B, max_pages) and table.is_contiguous()
+                and lengths.dtype is i32 and lengths.shape == rows[:1] and lengths.is_contiguous())
+        if fine:
+            here = _torch.cuda.current_device()
+            fine = (q.get_device() == here and out.get_device() == here and k_cache.get_device() == here and v_cache.get_device() == here
+                    and table.get_device() == here and lengths.get_device() == here
+                    and (fmt or k_d.get_device() == here and v_d.get_device() == here)
+                    and (workspace is None or workspace.get_device() == here and workspace.is_contiguous()))
+    except (AttributeError, KeyError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _wrong_cache(k_cache, v_cache, k_d, v_d)
+        B, Hq = q.shape[:2] if q is not None and q.dim() == 3 else (-1, -1)
+        D = k_cache.shape[3]
+        _wrong_rows(q, q.dtype if q is not None else None, (B, Hq, D), "q")
+        _wrong_dense(out, q.dtype, (B, Hq, D), "out")
+        _wrong_dense(table, _torch.int32, (B, table.shape[1] if table is not None and table.dim() == 2 else -1), "table")
+        _wrong_dense(lengths, _torch.int32, (B,), "lengths")
+        _wrong_device(q, k_cache, v_cache, table, lengths, out, k_d, v_d, workspace)
+        raise ValueError("q, out, the cache, table, lengths and workspace do not fit together (all but q contiguous)")
     if workspace is None:
         workspace = _workspace(nvq_attn_decode_workspace_bytes(B, Hq, heads, D, max_pages, page), stream, q)
-    wp, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
-    st = L.nvq_attn_decode(fmt, _row_types[dtype], q.data_ptr(), qs[0], qs[1], B, Hq, heads, D, kp, vp, kdp, vdp, n_pages, page, tp, max_pages, lp,
-                           D ** -0.5 if scale is None else scale, op, wp, ws_bytes, on)
+    wp, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = L.nvq_attn_decode(fmt, code, q.data_ptr(), qs[0], qs[1], B, Hq, heads, D, k_cache.data_ptr(), v_cache.data_ptr(),
+                           None if fmt else k_d.data_ptr(), None if fmt else v_d.data_ptr(), n_pages, page, table.data_ptr(), max_pages,
+                           lengths.data_ptr(), D ** -0.5 if scale is None else scale, out.data_ptr(), wp, ws_bytes,
+                           _torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream))
     if st:
         _check(st, "nvq_attn_decode")
 
@@ -764,18 +797,36 @@ def nvq_attn_prompt(q, k, v, cu_q, cu_k, out, scale=None, causal=True, stream=No
     -> out [Tq, Hq, D] (strides free).  Query i of m sees keys j <= i + n - m of its n (causal), else all.
     scale: 1 / sqrt(D) unless given."""
     L = _lib if _torch is not None else _attn_lib()
-    Tq, Hq, D = _row_shape(q, "q")
-    Tk, Hkv, _ = _row_shape(k, "k")
-    t = q.dtype
-    qs, ks, vs = _rows(q, t, (Tq, Hq, D), "q"), _rows(k, t, (Tk, Hkv, D), "k"), _rows(v, t, (Tk, Hkv, D), "v")
-    os_ = _rows(out, t, (Tq, Hq, D), "out")
-    if cu_q is None or cu_q.dim() != 1 or cu_q.shape[0] < 1:
-        raise ValueError("cu_q: int32 [B + 1] is required")
-    cq, ck = _dense(cu_q, _torch.int32, cu_q.shape, "cu_q"), _dense(cu_k, _torch.int32, cu_q.shape, "cu_k")
-    on = _on_device(stream, q, k, v, cu_q, cu_k, out)
-    strides = _Strides(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1])
-    st = L.nvq_attn_prompt(_row_types[t], q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), strides, cq, ck, cu_q.shape[0] - 1, Tq, Tk,
-                           Hq, Hkv, D, D ** -0.5 if scale is None else scale, 1 if causal else 0, on)
+    here = -1
+    try:
+        shape, keys, dtype, i32 = q.shape, k.shape, q.dtype, _torch.int32
+        (Tq, Hq, D), (Tk, Hkv, _) = shape, keys
+        qs, ks, vs, ps, n = q.stride(), k.stride(), v.stride(), out.stride(), cu_q.shape
+        fine = (dtype in _row_types and k.dtype is dtype and v.dtype is dtype and out.dtype is dtype and out.shape == shape and keys[2] == D
+                and v.shape == keys and qs[2] == ks[2] == vs[2] == ps[2] == 1 and len(n) == 1 and n[0] > 0 and cu_k.shape == n and cu_q.dtype is i32
+                and cu_k.dtype is i32 and cu_q.is_contiguous() and cu_k.is_contiguous())
+        if fine:
+            here = _torch.cuda.current_device()
+            fine = (q.get_device() == here and k.get_device() == here and v.get_device() == here and out.get_device() == here
+                    and cu_q.get_device() == here and cu_k.get_device() == here)
+    except (AttributeError, KeyError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        shape = tuple(q.shape) if q is not None and q.dim() == 3 else (-1, -1, -1)
+        _wrong_rows(q, q.dtype if q is not None else None, shape, "q")
+        keys = (*(k.shape[:2] if k is not None and k.dim() == 3 else (-1, -1)), shape[2])
+        for t, s, name in ((k, keys, "k"), (v, keys, "v"), (out, shape, "out")):
+            _wrong_rows(t, q.dtype, s, name)
+        if cu_q is None or cu_q.dim() != 1 or cu_q.shape[0] < 1:
+            raise ValueError("cu_q: int32 [B + 1] is required")
+        _wrong_dense(cu_q, _torch.int32, cu_q.shape, "cu_q")
+        _wrong_dense(cu_k, _torch.int32, cu_q.shape, "cu_k")
+        _wrong_device(q, k, v, cu_q, cu_k, out)
+        raise ValueError("q, k, v, out, cu_q and cu_k do not fit together")
+    strides = _Strides(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], ps[0], ps[1])
+    st = L.nvq_attn_prompt(_row_types[dtype], q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), strides, cu_q.data_ptr(), cu_k.data_ptr(),
+                           n[0] - 1, Tq, Tk, Hq, Hkv, D, D ** -0.5 if scale is None else scale, 1 if causal else 0,
+                           _torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream))
     if st:
         _check(st, "nvq_attn_prompt")
 
