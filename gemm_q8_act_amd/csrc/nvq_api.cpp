@@ -714,10 +714,11 @@ nvq_status nvq_kv_read(int fmt, int type, void* k, int64_t k_stride_t, int64_t k
                  k_cache, v_cache, k_d, v_d, n_pages, page, stream);
 }
 
-// One new token per sequence: the capacity in keys of all sequences has to fit an int.
+// One new token per sequence: the capacity in keys of all sequences stays below 2^30, so that
+// key numbers and rounded chunk lengths fit an int.
 static bool decode_shape_ok(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages, int64_t page) {
   return B >= 1 && B < kMaxDim && Hkv >= 1 && Hkv <= 65536 && Hq >= Hkv && Hq <= 65536 && Hq % Hkv == 0 && D >= 32 && D <= 256 &&
-         D % 32 == 0 && page_ok(page) && max_pages >= 1 && max_pages < kMaxDim / page && B < kMaxDim / (max_pages * page) &&
+         D % 32 == 0 && page_ok(page) && max_pages >= 1 && max_pages < kMaxDim / 2 / page && B * (max_pages * page) < kMaxDim / 2 &&
          nvq::attn_decode_groups(B, Hq, Hkv, max_pages * page) < kMaxDim;
 }
 
@@ -736,7 +737,7 @@ nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b,
   NVQ_TRY(check_cache(who, fmt, k_cache, v_cache, k_d, v_d, Hkv, D, n_pages, page, c));
   if (B == 0) return NVQ_OK;
   if (!decode_shape_ok(B, Hq, Hkv, D, max_pages, page))
-    return fail(NVQ_ERR_SHAPE, "%s: B=%lld, Hq=%lld, Hkv=%lld, max_pages=%lld, page=%lld out of range (Hq a multiple of Hkv, B * max_pages * page < 2^31)",
+    return fail(NVQ_ERR_SHAPE, "%s: B=%lld, Hq=%lld, Hkv=%lld, max_pages=%lld, page=%lld out of range (Hq a multiple of Hkv, B * max_pages * page < 2^30)",
                 who, (long long)B, (long long)Hq, (long long)Hkv, (long long)max_pages, (long long)page);
   if (!q || !table || !lengths || !out) return fail(NVQ_ERR_NULL, "%s: NULL pointer", who);
   NVQ_TRY(check_rows(who, "q", q, type, B, Hq, q_stride_b, q_stride_h));

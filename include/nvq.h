@@ -498,7 +498,7 @@ nvq_status nvq_kv_read(int fmt, int type, void* k, int64_t k_stride_t, int64_t k
  * with k_j, v_j the cache rows of key head h / (Hq/Hkv) at place j of sequence b: page
  * table[b][j / page], place j % page.  q [B][Hq][D] of `type` (strides between sequences and
  * between heads), out [B][Hq][D] of `type`, contiguous; table int32 [B][max_pages] and lengths
- * int32 [B] on the device.  Hq a multiple of Hkv; B * max_pages * page < 2^31.  A sequence
+ * int32 [B] on the device.  Hq a multiple of Hkv; B * max_pages * page < 2^30.  A sequence
  * of length 0 gives zeros; a length outside 0 .. max_pages * page, or a page number outside the
  * cache among its keys, gives NaN (nothing is read there).  Scores, sums and products are as
  * exact as float32 makes them (two binary16 terms, or three bfloat16 terms, of each float
@@ -521,7 +521,9 @@ nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b,
  * `type` NVQ_TYPE_F16 or BF16; strides[8]: token and head stride of q, k, v and out (host).
  * Hq a multiple of Hkv; Tq, Tk < 2^30; token strides of k and v below 2^24 elements.  Rows of out in no sequence are left alone; offsets
  * outside the tensors are cut to them.  Scores, softmax statistics and accumulation are
- * float32; the probabilities enter the second product rounded once to `type`. */
+ * float32; the probabilities enter the second product rounded once to `type`.  A value row
+ * with an infinity or NaN also makes non-finite those queries before it that share its tile of 64
+ * keys (0 times it is NaN); keys that a query does not see never matter. */
 nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v, void* out,
                            const int64_t* strides, const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq,
                            int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, float scale, int causal, void* stream);

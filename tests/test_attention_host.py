@@ -55,7 +55,7 @@ def test_read_refuses_rows_that_overlap(kw):
 @pytest.mark.parametrize("want,kw", [
     (NULL, dict(q=None)), (NULL, dict(table=None)), (NULL, dict(lengths=None)), (NULL, dict(out=None)), (NULL, dict(kc=None)), (NULL, dict(kd=None)),
     (RANGE, dict(fmt=9)), (RANGE, dict(type=5)), (RANGE, dict(fmt=2)), (SHAPE, dict(D=100)), (SHAPE, dict(Hq=41)), (SHAPE, dict(Hq=0)),
-    (SHAPE, dict(Hkv=0)), (SHAPE, dict(B=-1)), (SHAPE, dict(max_pages=0)), (SHAPE, dict(max_pages=1 << 30)), (SHAPE, dict(B=1 << 20, max_pages=1 << 6)),
+    (SHAPE, dict(Hkv=0)), (SHAPE, dict(B=-1)), (SHAPE, dict(max_pages=0)), (SHAPE, dict(max_pages=1 << 30)), (SHAPE, dict(max_pages=1 << 23)), (SHAPE, dict(B=1 << 20, max_pages=1 << 6)),
     (SHAPE, dict(page=24)), (ALIGN, dict(q=P + 8)), (ALIGN, dict(q_sb=5122)), (ALIGN, dict(out=P + 8)), (ALIGN, dict(table=P + 2)),
     (ALIGN, dict(lengths=P + 1)), (ALIGN, dict(ws=P + 8)), (WORKSPACE, dict(ws=None)), (WORKSPACE, dict(ws_bytes=100))])
 def test_decode_refusals(want, kw):
