@@ -49,27 +49,6 @@ __device__ __forceinline__ void store_pair(T* p, float a, float b) {
   *reinterpret_cast<uint32_t*>(p) = pack_pair<T>(a, b);
 }
 
-// 8 consecutive elements of a row of element type `type` (NVQ_TYPE_*, uniform), from element
-// `at` on; 16-byte aligned.
-__device__ __forceinline__ void load_8(const void* p, int type, int64_t at, float (&x)[8]) {
-  if (type == NVQ_TYPE_F32) {
-    const floatx4* s = reinterpret_cast<const floatx4*>(reinterpret_cast<const float*>(p) + at);
-    const floatx4 a = s[0], b = s[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = a[i], x[4 + i] = b[i];
-  } else {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(p) + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float t[2];
-      if (type == NVQ_TYPE_F16)
-        unpack_pair<_Float16>(w[i], t);
-      else
-        unpack_pair<__bf16>(w[i], t);
-      x[2 * i] = t[0], x[2 * i + 1] = t[1];
-    }
-  }
-}
 __device__ __forceinline__ void store_1(void* p, int type, int64_t at, float x) {
   if (type == NVQ_TYPE_F32)
     reinterpret_cast<float*>(p)[at] = x;
@@ -138,13 +117,9 @@ __device__ __forceinline__ int wave_running_sum(int v) {
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
-// 16 bytes a lane from base + offset straight into LDS, lane after lane from `lds` on; the
-// second form for what is read once (non-temporal), the third from an address a lane.  In
-// assembly because the compiler, which cannot tell one part of LDS from another, waits for
+// 16 bytes a lane from base + offset straight into LDS, lane after lane from `lds` on, of what
+// is read once (non-temporal); the second form from an address a lane.  In assembly because the compiler, which cannot tell one part of LDS from another, waits for
 // every such load before any LDS read; here the waits are written out (wait_loads).
-__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(lds) : "memory", "m0");
-}
 __device__ __forceinline__ void load_once_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(offset), "s"(base), "s"(lds) : "memory", "m0");
 }
@@ -183,6 +158,14 @@ __device__ __forceinline__ float add_pair(uint32_t v, float c) {
     return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, v), half2_t{(_Float16)1.0f, (_Float16)1.0f}, c, false);
   else
     return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, v), bf16x2_t{(__bf16)1.0f, (__bf16)1.0f}, c, false);
+}
+// c + 0 times both: c, or NaN if one of them is not finite
+template <typename T>
+__device__ __forceinline__ float zero_of_pair(uint32_t v, float c) {
+  if constexpr (__is_same(T, _Float16))
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, v), half2_t{(_Float16)0.0f, (_Float16)0.0f}, c, false);
+  else
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, v), bf16x2_t{(__bf16)0.0f, (__bf16)0.0f}, c, false);
 }
 
 // 2^x (v_exp_f32: about one unit in the last place; results below the normal range are 0)

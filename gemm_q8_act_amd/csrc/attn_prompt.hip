@@ -10,6 +10,16 @@
 // part of the second product's contraction, whose order is free: the probabilities go from
 // the softmax into the product without leaving their registers.  V^T's operands are read from
 // the row-major tile by the transposing LDS read (ds_read_b64_tr_b16).
+//
+// What bounds it: issue.  A wavefront's 64-key step is 8 D/32 products of 32 cycles, each beside
+// one exponential and about 4 other vector instructions (128 channels): 8192 tokens of
+// 40 heads of 128 over 8 key heads take 609 us, 1120 TFLOP/s, the matrix cores busy 59 % of it.
+// So a step's vector work (the softmax of tile t) stands beside products that do not depend on it
+// (the scores of tile t + 1), two wavefronts share a SIMD, and tiles come straight into LDS, which is
+// read for one product at a time.  32 queries a wavefront, since 64 do not fit the registers
+// (1980 us); all of a wavefront's keys by itself, since two wavefronts to 32 queries, every
+// other tile each, take 685 us (2048 tokens: 67 against 54; 256 tokens: 12.5 against 10.5).
+// Short prompts are latency: 256 tokens 10.5 us, of which 3 are start-up and 4 steps of 1.3.
 #include "attn_device.h"
 #include "nvq_launch.h"
 
@@ -35,7 +45,6 @@ struct PromptArgs {
   float scale_log2;  // not negative; the sign is in flip
   uint32_t flip;     // sign bits of a query pair
   int causal;
-
 };
 
 // Which head and which query tile (of all sequences) a workgroup takes.  Workgroups go round the
@@ -113,6 +122,49 @@ struct Stage {
   }
 };
 
+// Query `row_q` of a head by itself, out of memory and on the vector unit, for its keys 0 .. limit:
+// lanes take keys for the scores, pairs of channels for the result.  `m`: a maximum within 2^kSlack.
+template <typename T, int NB>
+__device__ __forceinline__ void one_query(const PromptArgs& a, const Span& sp, int head, int kvh, int row_q, int limit, float m) {
+  const int lane = (int)(threadIdx.x & 63);
+  const uint16_t* q = a.q + (int64_t)row_q * a.q_t + (int64_t)head * a.q_h;
+  constexpr int SETS = (NB + 3) / 4;  // pairs 64 x + lane
+  float acc[SETS][2] = {}, l = 0.0f;
+  for (int j0 = 0; j0 <= limit; j0 += 64) {
+    float p = 0.0f;
+    if (j0 + lane <= limit) {
+      const uint16_t* k = a.k + (int64_t)(sp.k0 + j0 + lane) * a.k_t + (int64_t)kvh * a.k_h;
+      float s = 0.0f;
+      for (int ch = 0; ch < 32 * NB; ch += 2) {
+        float x[2], y[2];
+        unpack_pair<T>(*reinterpret_cast<const uint32_t*>(q + ch) ^ a.flip, x);
+        unpack_pair<T>(*reinterpret_cast<const uint32_t*>(k + ch), y);
+        s = __builtin_fmaf(x[0], y[0], s), s = __builtin_fmaf(x[1], y[1], s);
+      }
+      float t[2];  // (rounded to the operand type as everywhere)
+      unpack_pair<T>(pack_pair<T>(exp2_fast(__builtin_fmaf(s, a.scale_log2, -m)), 0.0f), t);
+      p = t[0];
+    }
+    const int some = min(64, limit - j0 + 1);
+    for (int jj = 0; jj < some; ++jj) {
+      const float pj = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, p), jj));
+      const uint16_t* v = a.v + (int64_t)(sp.k0 + j0 + jj) * a.v_t + (int64_t)kvh * a.v_h;
+      l += pj;
+#pragma unroll
+      for (int x = 0; x < SETS; ++x)
+        if (64 * x + lane < 16 * NB) {
+          float y[2];
+          unpack_pair<T>(*reinterpret_cast<const uint32_t*>(v + 2 * (64 * x + lane)), y);
+          acc[x][0] = __builtin_fmaf(pj, y[0], acc[x][0]), acc[x][1] = __builtin_fmaf(pj, y[1], acc[x][1]);
+        }
+    }
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* out = a.out + (int64_t)row_q * a.o_t + (int64_t)head * a.o_h;
+#pragma unroll
+  for (int x = 0; x < SETS; ++x)
+    if (64 * x + lane < 16 * NB) *reinterpret_cast<uint32_t*>(out + 2 * (64 * x + lane)) = pack_pair<T>(acc[x][0] * inv, acc[x][1] * inv);
+}
 
 template <typename T, int NB>
 __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kernel(PromptArgs a) {
@@ -286,6 +338,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
   // only load their share.
   const auto turn = [&]() __attribute__((always_inline)) {
     wait_loads<0>();
+    wait_reads();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
@@ -316,15 +369,30 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
   }
 
   l = sum_32(l);
-  if (i >= sp.m) return;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a query that sees no key gives zeros
-  uint16_t* row = a.out + (int64_t)(sp.q0 + i) * a.o_t + (int64_t)head * a.o_h;
+  // A value that is not finite, in a row that a query does not see but whose tile it takes part
+  // in, has made 0 times it, NaN, of the query's sum.  So a query with numbers for its
+  // probabilities and none for its result is done again by itself.  (The test behind the stores, in
+  // four chains, is hidden: 256 tokens 10.5 us with and without it; in front of them 10.9.)
+  float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // 0, or NaN if any result is not finite
+  uint16_t* row = a.out + (int64_t)(sp.q0 + min(i, sp.m - 1)) * a.o_t + (int64_t)head * a.o_h;
 #pragma unroll
   for (int t = 0; t < NB; ++t)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<u32x2*>(row + 32 * t + 8 * j + 4 * hi) =
-          u32x2{pack_pair<T>(acc[t][4 * j] * inv, acc[t][4 * j + 1] * inv), pack_pair<T>(acc[t][4 * j + 2] * inv, acc[t][4 * j + 3] * inv)};
+    for (int j = 0; j < 4; ++j) {
+      const u32x2 w = {pack_pair<T>(acc[t][4 * j] * inv, acc[t][4 * j + 1] * inv), pack_pair<T>(acc[t][4 * j + 2] * inv, acc[t][4 * j + 3] * inv)};
+      if (i < sp.m) *reinterpret_cast<u32x2*>(row + 32 * t + 8 * j + 4 * hi) = w;
+      z[j] = zero_of_pair<T>(w[1], zero_of_pair<T>(w[0], z[j]));
+    }
+  const float none = (z[0] + z[1]) + (z[2] + z[3]);
+  const uint64_t broken = __ballot(a.causal && i < sp.m && l == l && none != none);
+  uint32_t again = (uint32_t)broken | (uint32_t)(broken >> 32);
+  if (again) wait_loads<0>();  // (for the stores: the rows are written over)
+  for (; again; again &= again - 1) {
+    const int x = __builtin_ctz(again);
+    const float m_x = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, m), x));
+    one_query<T, NB>(a, sp, head, kvh, sp.q0 + iw + x, min(iw + x + shift, sp.n - 1), m_x == -__builtin_inff() ? 0.0f : m_x);
+  }
 }
 
 template <typename T, int NB>

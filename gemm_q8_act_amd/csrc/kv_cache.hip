@@ -7,8 +7,10 @@
 // contiguous bytes a block, and the lane's codes are the 2 D/32 consecutive bytes that
 // the quantised row's element order gives it (nvq.h): one wide store.
 //
-// HBM-bound: D * (element bytes + 34/32) a row, each byte once.  Keys and values go in one
-// launch: a decode step writes a few rows and is all launch.
+// HBM-bound: D * (element bytes + 34/32) a row, each byte once; 16411 tokens of 8 key heads of
+// 128, bfloat16 to Q8_0: written in 25.5 us (4.0 TB/s), read in 20 us (5.2 TB/s; a large copy
+// 4.75).  Keys and values go in one launch: a decode step writes a few rows and is all launch (one
+// token: 2.6 us written, 1.8 read).
 #include "attn_device.h"
 #include "nvq_launch.h"
 

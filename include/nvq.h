@@ -519,11 +519,12 @@ nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b,
  * keys, query i sees keys j <= i + n - m if causal (the last query sees all: n > m puts the
  * queries behind n - m keys of a prefix), else all n.  A query that sees no key gives zeros.
  * `type` NVQ_TYPE_F16 or BF16; strides[8]: token and head stride of q, k, v and out (host).
- * Hq a multiple of Hkv; Tq, Tk < 2^30; token strides of k and v below 2^24 elements.  Rows of out in no sequence are left alone; offsets
- * outside the tensors are cut to them.  Scores, softmax statistics and accumulation are
- * float32; the probabilities enter the second product rounded once to `type`.  A value row
- * with an infinity or NaN also makes non-finite those queries before it that share its tile of 64
- * keys (0 times it is NaN); keys that a query does not see never matter. */
+ * Hq a multiple of Hkv; Tq, Tk < 2^30; token strides of k and v below 2^24 elements.  Rows of
+ * out in no sequence are left alone; offsets outside the tensors are cut to them.  Scores,
+ * softmax statistics and accumulation are float32; the probabilities enter the second product
+ * rounded once to `type`.  Keys and values that a query does not see never matter, whatever they
+ * hold (queries that an infinity or NaN in such a value row of their tile would reach are done
+ * one by one, slowly). */
 nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v, void* out,
                            const int64_t* strides, const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq,
                            int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, float scale, int causal, void* stream);

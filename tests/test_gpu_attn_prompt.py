@@ -112,6 +112,31 @@ def test_strides_and_rows_outside_the_sequences():
     assert (out[:7] == 7).all() and (out[7 + q.shape[0]:] == 7).all()
 
 
+@pytest.mark.parametrize("type_", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [32, 64, 128, 160, 256])
+def test_non_finite_rows_reach_only_queries_that_see_them(D, type_):
+    """An infinity or NaN in one channel of a value row shows in that channel of the queries that see the row, in a key
+    row in all of theirs; queries before it in the same tile, and those that see no key, are as if it were not there."""
+    q, k, v, cu_q, cu_k = make([(200, 260), (40, 30), (70, 70)], 4, 2, D, type_, 17 + D)
+    for row, ch, x in ((63, 1, np.inf), (130, 3, np.nan), (259, 5, np.inf), (262, 0, np.nan), (359, 31, -np.inf)):
+        v[row, :, ch] = x
+    k[350, 1, 7] = np.nan
+    got = host(call(*(on_gpu(a, type_) for a in (q, k, v)), cu_q, cu_k).float())
+    for b in range(3):
+        a, e, x, y = cu_q[b], cu_q[b + 1], cu_k[b], cu_k[b + 1]
+        m, n = e - a, y - x
+        seen = np.arange(n)[None] <= np.arange(m)[:, None] + (n - m)
+        for h in range(4):
+            with np.errstate(invalid="ignore"):
+                want, A, S = attention(q[a:e, h], k[x:y, h // 2], v[x:y, h // 2], D ** -0.5, seen)
+                limit = bound(want, A, S, D, n, type_, HALF_UNIT[type_], 2)
+            ok = np.isfinite(want)
+            assert (np.isfinite(got[a:e, h]) == ok).all(), f"sequence {b} head {h}"
+            assert (np.isnan(got[a:e, h]) == np.isnan(want)).all() and (got[a:e, h][np.isinf(want)] == want[np.isinf(want)]).all()
+            assert (np.abs(got[a:e, h] - want)[ok] <= limit[ok]).all(), f"sequence {b} head {h}"
+            assert 0 < ok.sum() < ok.size and (got[a:e, h][~seen.any(1)] == 0).all()
+
+
 def test_offsets_outside_the_tensors_are_cut():
     torch = torch_dev()
     q, k, v, cu_q, cu_k = make([(40, 40)], 2, 1, 64, "f16", 14)
