@@ -524,7 +524,7 @@ nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b,
  * softmax statistics and accumulation are float32; the probabilities enter the second product
  * rounded once to `type`.  Keys and values that a query does not see never matter, whatever they
  * hold (queries that an infinity or NaN in such a value row of their tile would reach are done
- * one by one, slowly). */
+ * one by one, slowly).  out overlaps none of the inputs. */
 nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v, void* out,
                            const int64_t* strides, const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq,
                            int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, float scale, int causal, void* stream);

@@ -137,6 +137,21 @@ def test_non_finite_rows_reach_only_queries_that_see_them(D, type_):
             assert 0 < ok.sum() < ok.size and (got[a:e, h][~seen.any(1)] == 0).all()
 
 
+@pytest.mark.parametrize("x", [np.inf, np.nan])
+def test_non_finite_channel(x):
+    """One channel of every value row: it alone is that in every result, and zero where no key is seen."""
+    q, k, v, cu_q, cu_k = make([(150, 150), (40, 20)], 2, 1, 96, "bf16", 18)
+    want = host(call(*(on_gpu(a, "bf16") for a in (q, k, v)), cu_q, cu_k).float())
+    v[:, :, 37] = x
+    got = host(call(*(on_gpu(a, "bf16") for a in (q, k, v)), cu_q, cu_k).float())
+    assert (got[170:, :, 37] == x).all() or np.isnan(x) and np.isnan(got[170:, :, 37]).all()
+    assert (got[:150, :, 37] == x).all() or np.isnan(x) and np.isnan(got[:150, :, 37]).all()
+    assert (got[150:170] == 0).all()
+    rest = np.arange(96) != 37
+    # (rounded at two maxima at most 2^8 apart: twice the half unit of a probability, and the result's own)
+    assert np.abs(got - want)[..., rest].max() <= 4 * HALF_UNIT["bf16"] * np.abs(v[..., rest]).max()
+
+
 def test_offsets_outside_the_tensors_are_cut():
     torch = torch_dev()
     q, k, v, cu_q, cu_k = make([(40, 40)], 2, 1, 64, "f16", 14)
