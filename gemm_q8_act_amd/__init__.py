@@ -633,13 +633,16 @@ _cache_types: dict = {}  # torch dtype -> NVQ_KV_*
 
 
 def _attn_lib():
+    """The library, loaded if it was not; the entries take _lib by itself once _torch says that both are there, so
+    that is set last."""
     global _torch
     import torch
 
+    L = lib()
     _row_types.update({torch.float32: NVQ_TYPE_F32, torch.float16: NVQ_TYPE_F16, torch.bfloat16: NVQ_TYPE_BF16})
     _cache_types.update({torch.int8: NVQ_KV_Q8_0, torch.float16: NVQ_KV_F16, torch.bfloat16: NVQ_KV_BF16})
     _torch = torch
-    return lib()
+    return L
 
 
 def _wrong_rows(t, dtype, shape, name):

@@ -1,0 +1,64 @@
+"""The cache and attention entries' binding, without a GPU: its first call, from one thread and from several."""
+import threading
+
+import pytest
+
+import gemm_q8_act_amd as nvq
+
+
+def _refused():
+    """A call that gets past the library and is refused for its arguments."""
+    import torch
+
+    x = torch.zeros((3, 1, 32))
+    c, d = torch.zeros((2, 1, 16, 32), dtype=torch.int8), torch.zeros((2, 1, 16, 1), dtype=torch.float16)
+    nvq.nvq_kv_write(x.double(), x, torch.zeros(3, dtype=torch.int64), c, c, d, d)
+
+
+@pytest.fixture
+def unloaded(monkeypatch):
+    real = nvq.lib()
+    monkeypatch.setattr(nvq, "_lib", None)
+    monkeypatch.setattr(nvq, "_torch", None)
+    return real
+
+
+def test_a_library_that_cannot_be_loaded_is_named_every_time(unloaded, monkeypatch):
+    def missing():
+        raise ImportError("libnvq.so not built")
+
+    monkeypatch.setattr(nvq, "lib", missing)
+    for _ in range(2):
+        with pytest.raises(ImportError, match="not built"):
+            _refused()
+
+
+def test_first_calls_of_several_threads(unloaded, monkeypatch):
+    """A second thread's first call while the library is loading waits for it as the first one's does."""
+    inside, go = threading.Event(), threading.Event()
+
+    def slow():
+        inside.set()
+        assert go.wait(30)
+        nvq._lib = unloaded
+        return unloaded
+
+    monkeypatch.setattr(nvq, "lib", slow)
+    errors = []
+
+    def call():
+        try:
+            _refused()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=call) for _ in range(4)]
+    threads[0].start()
+    assert inside.wait(30)
+    for t in threads[1:]:
+        t.start()
+    threads[1].join(1.0)  # what would not wait for the library has ended by then
+    go.set()
+    for t in threads:
+        t.join(30)
+    assert len(errors) == 4 and all(type(e) is ValueError for e in errors), errors
