@@ -785,14 +785,15 @@ def nvq_attn_decode(q, k_cache, v_cache, table, lengths, out, k_d=None, v_d=None
 
 
 def _workspace(nbytes, stream, like):
-    """Scratch of one call.  torch's allocator hands it out again in the order of the stream that it was allocated
-    on, so on a stream of the caller's it has to be told of that one."""
+    """Scratch of one call, asked for with the call's stream current: torch's allocator hands memory out again in the
+    order of the stream that it was asked for on, so a block that work waiting on another stream has just
+    let go of is not it."""
     if not nbytes:
         return None
-    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=like.device)
-    if stream is not None and int(stream) != _torch.cuda.current_stream(like.device).cuda_stream:
-        ws.record_stream(_torch.cuda.ExternalStream(int(stream), device=like.device))
-    return ws
+    if stream is None or int(stream) == _torch.cuda.current_stream(like.device).cuda_stream:
+        return _torch.empty(nbytes, dtype=_torch.uint8, device=like.device)
+    with _torch.cuda.stream(_torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream) else _torch.cuda.default_stream(like.device)):
+        return _torch.empty(nbytes, dtype=_torch.uint8, device=like.device)
 
 
 def nvq_attn_prompt(q, k, v, cu_q, cu_k, out, scale=None, causal=True, stream=None) -> None:

@@ -62,3 +62,35 @@ def test_first_calls_of_several_threads(unloaded, monkeypatch):
     for t in threads:
         t.join(30)
     assert len(errors) == 4 and all(type(e) is ValueError for e in errors), errors
+
+
+@pytest.mark.parametrize("stream,want", [(None, 77), (77, 77), (5, 5), (0, 0)])
+def test_scratch_comes_from_the_stream_that_uses_it(monkeypatch, stream, want):
+    """torch's allocator hands memory out in the order of the stream that is current when it is asked: scratch of a call
+    on another stream has to be asked for there, or work still waiting on the current one writes over it."""
+    import contextlib
+    import types
+
+    import torch
+
+    current, asked = [77], []
+
+    @contextlib.contextmanager
+    def on(s):
+        current.append(s.cuda_stream)
+        yield
+        current.pop()
+
+    def empty(n, dtype, device):
+        asked.append((n, current[-1], device))
+        return types.SimpleNamespace(record_stream=lambda s: None)
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: types.SimpleNamespace(cuda_stream=current[-1]))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda d=None: types.SimpleNamespace(cuda_stream=0))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda p, device=None: types.SimpleNamespace(cuda_stream=p))
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(nvq, "_torch", torch)
+    assert nvq._workspace(4096, stream, types.SimpleNamespace(device="cuda:0")) is not None
+    assert asked == [(4096, want, "cuda:0")] and current == [77]
+    assert nvq._workspace(0, stream, None) is None
