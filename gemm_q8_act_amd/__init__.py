@@ -179,6 +179,20 @@ def _need(t, dtype, shape, name):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _workspace(nbytes, stream, like):
+    """Scratch of one call, asked for with the call's stream current: torch's allocator hands memory out again in the
+    order of the stream that it was asked for on, so a block that work waiting on another stream has just
+    let go of is not it."""
+    if not nbytes:
+        return None
+    import torch
+
+    if stream is None or int(stream) == torch.cuda.current_stream(like.device).cuda_stream:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream) else torch.cuda.default_stream(like.device)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
 # ---------------------------------------------------------------------------
 # sizes and packers (host)
 # ---------------------------------------------------------------------------
@@ -340,9 +354,7 @@ def nvq_gemm_nvfp4(w, w_scale: float, q, d_f16, y, workspace=None, stream=None) 
     _need(y, torch.float32, (M, N), "y")
     _weights(w, nvq_nvfp4_weight_bytes(N, K), "w")
     if workspace is None:  # the split-K partial tiles; torch's caching allocator makes this cheap
-        need = lib().nvq_gemm_workspace_bytes(NVQ_FMT_NVFP4, M, N, K)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=y.device)
+        workspace = _workspace(lib().nvq_gemm_workspace_bytes(NVQ_FMT_NVFP4, M, N, K), stream, y)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().nvq_gemm_nvfp4(_ptr(w), float(w_scale), _ptr(q), _ptr(d_f16), M, N, K, _ptr(y),
                                 _ptr(workspace), ws_bytes, _stream(stream, y)), "nvq_gemm_nvfp4")
@@ -382,9 +394,7 @@ def nvq_gemm_q4_1(w, q, d_f16, bsum16, y, workspace=None, stream=None) -> None:
     _need(bsum16, torch.int16, (M, K // 16), "bsum16")
     _weights(w, nvq_q4_1_weight_bytes(N, K), "w")
     if workspace is None:
-        need = lib().nvq_gemm_workspace_bytes(NVQ_FMT_Q4_1, M, N, K)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=y.device)
+        workspace = _workspace(lib().nvq_gemm_workspace_bytes(NVQ_FMT_Q4_1, M, N, K), stream, y)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().nvq_gemm_q4_1(_ptr(w), _ptr(q), _ptr(d_f16), _ptr(bsum16), M, N, K, _ptr(y),
                                _ptr(workspace), ws_bytes, _stream(stream, y)), "nvq_gemm_q4_1")
@@ -432,9 +442,7 @@ def nvq_gemm_q4_k(w, q, d_f16, bsum16, y, workspace=None, stream=None) -> None:
     _need(bsum16, torch.int16, (M, K // 16), "bsum16")
     _weights(w, nvq_q4_k_weight_bytes(N, K), "w")
     if workspace is None:
-        need = lib().nvq_gemm_workspace_bytes(NVQ_FMT_Q4_K, M, N, K)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=y.device)
+        workspace = _workspace(lib().nvq_gemm_workspace_bytes(NVQ_FMT_Q4_K, M, N, K), stream, y)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().nvq_gemm_q4_k(_ptr(w), _ptr(q), _ptr(d_f16), _ptr(bsum16), M, N, K, _ptr(y),
                                _ptr(workspace), ws_bytes, _stream(stream, y)), "nvq_gemm_q4_k")
@@ -506,9 +514,7 @@ def nvq_gemm_q5_k(w, q, d_f16, bsum16, y, workspace=None, stream=None) -> None:
     _need(bsum16, torch.int16, (M, K // 16), "bsum16")
     _weights(w, nvq_q5_k_weight_bytes(N, K), "w")
     if workspace is None:
-        need = lib().nvq_gemm_workspace_bytes(NVQ_FMT_Q5_K, M, N, K)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=y.device)
+        workspace = _workspace(lib().nvq_gemm_workspace_bytes(NVQ_FMT_Q5_K, M, N, K), stream, y)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().nvq_gemm_q5_k(_ptr(w), _ptr(q), _ptr(d_f16), _ptr(bsum16), M, N, K, _ptr(y),
                                _ptr(workspace), ws_bytes, _stream(stream, y)), "nvq_gemm_q5_k")
@@ -533,9 +539,7 @@ def nvq_gemm_q6_k(w, q, d_f16, y, workspace=None, stream=None) -> None:
     _need(y, torch.float32, (M, N), "y")
     _weights(w, nvq_q6_k_weight_bytes(N, K), "w")
     if workspace is None:
-        need = lib().nvq_gemm_workspace_bytes(NVQ_FMT_Q6_K, M, N, K)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=y.device)
+        workspace = _workspace(lib().nvq_gemm_workspace_bytes(NVQ_FMT_Q6_K, M, N, K), stream, y)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().nvq_gemm_q6_k(_ptr(w), _ptr(q), _ptr(d_f16), M, N, K, _ptr(y), _ptr(workspace), ws_bytes,
                                _stream(stream, y)), "nvq_gemm_q6_k")
@@ -585,9 +589,7 @@ def nvq_gemm_iq4_xs(w, table, q, d_f16, y, workspace=None, stream=None) -> None:
     _need(y, torch.float32, (M, N), "y")
     _weights(w, nvq_iq4_xs_weight_bytes(N, K), "w")
     if workspace is None:
-        need = lib().nvq_gemm_workspace_bytes(NVQ_FMT_IQ4_XS, M, N, K)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=y.device)
+        workspace = _workspace(lib().nvq_gemm_workspace_bytes(NVQ_FMT_IQ4_XS, M, N, K), stream, y)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().nvq_gemm_iq4_xs(_ptr(w), t.ctypes.data_as(ctypes.c_void_p), _ptr(q), _ptr(d_f16), M, N, K, _ptr(y),
                                  _ptr(workspace), ws_bytes, _stream(stream, y)), "nvq_gemm_iq4_xs")
@@ -782,18 +784,6 @@ def nvq_attn_decode(q, k_cache, v_cache, table, lengths, out, k_d=None, v_d=None
                            _torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream))
     if st:
         _check(st, "nvq_attn_decode")
-
-
-def _workspace(nbytes, stream, like):
-    """Scratch of one call, asked for with the call's stream current: torch's allocator hands memory out again in the
-    order of the stream that it was asked for on, so a block that work waiting on another stream has just
-    let go of is not it."""
-    if not nbytes:
-        return None
-    if stream is None or int(stream) == _torch.cuda.current_stream(like.device).cuda_stream:
-        return _torch.empty(nbytes, dtype=_torch.uint8, device=like.device)
-    with _torch.cuda.stream(_torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream) else _torch.cuda.default_stream(like.device)):
-        return _torch.empty(nbytes, dtype=_torch.uint8, device=like.device)
 
 
 def nvq_attn_prompt(q, k, v, cu_q, cu_k, out, scale=None, causal=True, stream=None) -> None:
