@@ -12,8 +12,9 @@
 // free: the probabilities never leave their registers.
 //
 // Types.  Scores and results are as exact as float32 arithmetic makes them: the float
-// operands (q and P) go in as the sum of two binary16 terms (22 bits) or three bfloat16 terms
-// (24 bits), accumulated in float32.  Q8_0 codes are whole numbers, exact in either type:
+// operands (q and P) go in as the sum of two binary16 terms (22 bits; a query's channels are held to
+// 2^-32 of its largest at least, a P too small for them goes another way) or three bfloat16
+// terms (24 bits), accumulated in float32.  Q8_0 codes are whole numbers, exact in either type:
 // a block's 32 channels are one instruction's contraction over the keys' codes, whose scale
 // multiplies the block's sum in float32; the value scale goes into P.
 //
@@ -46,9 +47,13 @@ constexpr int kTargetGroups = 512;
 constexpr int kJoinWaves = 8;
 // A score may pass the running maximum by 2^kSlack before everything is rescaled.
 constexpr float kSlack = 8.0f;
-// Over a binary16 cache P (at most 2^kSlack) goes in times this: the largest stays inside
-// binary16, and one of 2^-21 is still a normal number there.
-constexpr float kHalfScale = 128.0f;
+// Over a binary16 cache P (at most 2^kSlack) goes in times kHalfScale, as two binary16 terms: the
+// largest stays inside binary16, and 2^-20 of any P from kHalfLeast on is held.  Smaller ones lose
+// bits and vanish below 2^-32, and behind a heavy key whose values are 0 what they add is the
+// whole result; so a tile that has one goes in as bfloat16 terms, of P and of the values, which hold
+// float32's range (5 products for 2).  64 x <= 8192 keys, 8 key heads of 128: 190 us with few such tiles
+// (scores of width 1), 205 with most (width 3 and more); 16 x <= 2000, 16 of 64: 20.9 and 23.9.
+constexpr float kHalfScale = 128.0f, kHalfLeast = 0x1p-12f;
 
 struct DecodeArgs {
   const void* q;
@@ -190,6 +195,16 @@ __device__ __forceinline__ float half_of(const uint32_t* w, int i) {
 __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t a, uint32_t b, int i) {
   const float x = (float)(int)(int8_t)(a >> (8 * i)), y = (float)(int)(int8_t)(b >> (8 * i));
   return perm(__builtin_bit_cast(uint32_t, y), __builtin_bit_cast(uint32_t, x), 0x07060302u);
+}
+
+// A binary16 pair as two bfloat16 pairs whose sum it is: the upper 8 of its 11 bits, and the rest.
+__device__ __forceinline__ void halves_to_bf16(uint32_t v, uint32_t& top, uint32_t& rest) {
+  float x[2];
+  unpack_pair<_Float16>(v, x);
+  const uint32_t a = __builtin_bit_cast(uint32_t, x[0]), b = __builtin_bit_cast(uint32_t, x[1]);
+  top = perm(b, a, 0x07060302u);
+  rest = perm(__builtin_bit_cast(uint32_t, x[1] - __builtin_bit_cast(float, b & 0xFFFF0000u)),
+              __builtin_bit_cast(uint32_t, x[0] - __builtin_bit_cast(float, a & 0xFFFF0000u)), 0x07060302u);
 }
 
 // Eight floats as the sum of TERMS 16-bit operands, each the rounding of what the ones before
@@ -502,10 +517,6 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES), (Shape<FMT, NB>::EU_W
       p[i] = exp2_fast(sc[i] - m_safe);
       l += p[i];
     }
-    if constexpr (FMT == NVQ_KV_F16) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] *= kHalfScale;
-    }
     if constexpr (S::Q8) {
 #pragma unroll
       for (int set = 0; set < SETS; ++set) {
@@ -525,16 +536,44 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES), (Shape<FMT, NB>::EU_W
         }
       }
     } else {
-      Frag pf[S::P_TERMS];
-      split_terms<typename S::P, S::P_TERMS>(p, pf);
-#pragma unroll
-      for (int i = 0; i < S::TILES; ++i) {  // channels 2 NB n + i
+      const auto values = [&](int i) __attribute__((always_inline)) {  // channels 2 NB n + i
         Frag f;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           f.v[j] = perm(vw[j >> 1][2 * (j & 1) + 1][i >> 1], vw[j >> 1][2 * (j & 1)][i >> 1], i & 1 ? 0x07060302u : 0x05040100u);
+        return f;
+      };
+      bool small = false;
+      if constexpr (FMT == NVQ_KV_F16) {
+        uint32_t least = ~0u;  // of the P that are not 0: its bits, less 1
 #pragma unroll
-        for (int k = 0; k < S::P_TERMS; ++k) acc[i] = mfma16<typename S::P>(f, pf[k], acc[i]);
+        for (int i = 0; i < 8; ++i) least = min(least, __builtin_bit_cast(uint32_t, p[i]) - 1u);
+        small = __any(least < __builtin_bit_cast(uint32_t, kHalfLeast) - 1u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] *= kHalfScale;
+      }
+      if (!small) {
+        Frag pf[S::P_TERMS];
+        split_terms<typename S::P, S::P_TERMS>(p, pf);
+#pragma unroll
+        for (int i = 0; i < S::TILES; ++i) {
+          const Frag f = values(i);
+#pragma unroll
+          for (int k = 0; k < S::P_TERMS; ++k) acc[i] = mfma16<typename S::P>(f, pf[k], acc[i]);
+        }
+      } else {
+        Frag pf[3];
+        split_terms<__bf16, 3>(p, pf);
+#pragma unroll
+        for (int i = 0; i < S::TILES; ++i) {
+          Frag f = values(i), rest;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) halves_to_bf16(f.v[j], f.v[j], rest.v[j]);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) acc[i] = mfma16<__bf16>(f, pf[k], acc[i]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) acc[i] = mfma16<__bf16>(rest, pf[k], acc[i]);  // (the third: below 2^-25 of it all)
+        }
       }
     }
   }

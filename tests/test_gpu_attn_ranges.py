@@ -1,0 +1,53 @@
+"""Attention whose probabilities or values reach far: heavy keys whose values are zero, so that what is left is
+the sum of small probabilities.  The bounds are those of every other test: each probability to the
+rounding that its operator states, whatever its size."""
+import numpy as np
+import pytest
+
+from attn_cases import Paged, attention, bound, check
+from gpu_cases import host, say, torch_dev
+
+pytestmark = pytest.mark.gpu
+
+
+def far_rows(r, n, H, D, at, gap):
+    """Rows k, v of which row `at` stands `gap` nats before the others for a query whose channel 0 is 1 (scale 1), and
+    has values of zero."""
+    k, v = (r.standard_normal((n, H, D)).astype(np.float32) for _ in "kv")
+    k *= 0.25
+    k[:, :, 0] = 0.0
+    k[at] = 0.0
+    k[at, :, 0] = gap
+    v[at] = 0.0
+    return k, v
+
+
+def queries(r, n, H, D):
+    q = (r.standard_normal((n, H, D)) * 0.25).astype(np.float32)
+    q[:, :, 0] = 1.0
+    return q
+
+
+def decode(fmt, seqs, q, D, page, seed, what, heads):
+    torch = torch_dev()
+    Hq, Hkv = q.shape[1], seqs[0][0].shape[1]
+    c = Paged(fmt, seqs, Hkv, D, page, seed)
+    got = host(c.decode(torch.from_numpy(q).cuda(), scale=1.0))
+    worst = 0.0
+    for i, (k, v) in enumerate(c.rows):
+        for h in heads:
+            j = h * Hkv // Hq
+            want, A, S = attention(q[i, h:h + 1], k[:, j], v[:, j], 1.0, np.ones((1, len(k)), bool))
+            worst = max(worst, check(got[i, h:h + 1], want, bound(want, A, S, D, len(k), "f32", 0.0, 8), f"{what} sequence {i} head {h}"))
+    say(f"  worst error / bound {worst:.3g}")
+
+
+@pytest.mark.parametrize("fmt", ["q8_0", "f16", "bf16"])
+@pytest.mark.parametrize("gap", [8, 15, 20, 30, 60])
+def test_decode_small_probabilities(fmt, gap):
+    """The heavy key first, in the middle and last; 4200 keys in long parts (many key heads) and 601 in short ones."""
+    say(f"decode small probabilities {fmt} gap={gap}")
+    r = np.random.Generator(np.random.PCG64(gap))
+    for n, Hkv, Hq, D, places, heads in ((601, 2, 4, 64, (0, 311, 600), range(4)), (4200, 64, 64, 32, (0, 2100, 4199), (0, 31, 63))):
+        seqs = [far_rows(r, n, Hkv, D, at, gap) for at in places]
+        decode(fmt, seqs, queries(r, len(seqs), Hq, D), D, 16, gap + n, f"{fmt} gap {gap}", heads)
