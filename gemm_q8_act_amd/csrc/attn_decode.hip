@@ -47,6 +47,9 @@ constexpr int kTargetGroups = 512;
 constexpr int kJoinWaves = 8;
 // A score may pass the running maximum by 2^kSlack before everything is rescaled.
 constexpr float kSlack = 8.0f;
+// Over a bfloat16 cache P and its sum are taken times this, so that P is at most 1: values reach to the
+// top of float32, and times 2^kSlack they would pass it where the result does not.
+constexpr float kTopScale = 0x1p-8f;
 // Over a binary16 cache P (at most 2^kSlack) goes in times kHalfScale, as two binary16 terms: the
 // largest stays inside binary16, and 2^-20 of any P from kHalfLeast on is held.  Smaller ones lose
 // bits and vanish below 2^-32, and behind a heavy key whose values are 0 what they add is the
@@ -515,6 +518,7 @@ __global__ __launch_bounds__((64 * Shape<FMT, NB>::WAVES), (Shape<FMT, NB>::EU_W
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       p[i] = exp2_fast(sc[i] - m_safe);
+      if constexpr (FMT == NVQ_KV_BF16) p[i] *= kTopScale;
       l += p[i];
     }
     if constexpr (S::Q8) {

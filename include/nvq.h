@@ -502,7 +502,7 @@ nvq_status nvq_kv_read(int fmt, int type, void* k, int64_t k_stride_t, int64_t k
  * of length 0 gives zeros; a length outside 0 .. max_pages * page, or a page number outside the
  * cache among its keys, gives NaN (nothing is read there).  Scores, sums and products are as
  * exact as float32 makes them (two binary16 terms, or three bfloat16 terms, of each float
- * operand; float32 accumulation; probabilities down to 2^-120 of the largest count; over a Q8_0
+ * operand; float32 accumulation; probabilities down to 2^-100 of the largest count; over a Q8_0
  * or binary16 cache a query's channels are held to 2^-20 of themselves or 2^-32 of its largest
  * one, whichever is more); out is rounded once.  Non-finite values among a sequence's
  * keys or values give non-finite results.

@@ -1,6 +1,6 @@
 """Attention whose probabilities or values reach far: heavy keys whose values are zero, so that what is left is
-the sum of small probabilities.  The bounds are those of every other test: each probability to the
-rounding that its operator states, whatever its size."""
+the sum of small probabilities, and values near the top of bfloat16.  The bounds are those of
+every other test: each probability to the rounding that its operator states, whatever its size."""
 import numpy as np
 import pytest
 
@@ -51,3 +51,16 @@ def test_decode_small_probabilities(fmt, gap):
     for n, Hkv, Hq, D, places, heads in ((601, 2, 4, 64, (0, 311, 600), range(4)), (4200, 64, 64, 32, (0, 2100, 4199), (0, 31, 63))):
         seqs = [far_rows(r, n, Hkv, D, at, gap) for at in places]
         decode(fmt, seqs, queries(r, len(seqs), Hq, D), D, 16, gap + n, f"{fmt} gap {gap}", heads)
+
+
+def test_decode_values_near_the_top_of_bfloat16():
+    """Every weighted sum with probabilities up to 1 fits float32 (5000 values below 2^114); scores rise by 7.8 powers of two
+    after the first tile, which is less than the running maximum follows at once."""
+    say("decode values of 2^113 .. 2^114")
+    r = np.random.Generator(np.random.PCG64(4))
+    n, Hkv, D = 5000, 64, 32
+    k = (r.standard_normal((n, Hkv, D)) * 2.0 ** -6).astype(np.float32)
+    k[:, :, 0] = 5.375
+    k[:128, :, 0] = 0.0
+    v = (r.uniform(0.5, 0.99, (n, Hkv, D)) * 2.0 ** 114).astype(np.float32)
+    decode("bf16", [(k, v)], queries(r, 1, Hkv, D), D, 64, 5, "large values", (0, 17, 63))
