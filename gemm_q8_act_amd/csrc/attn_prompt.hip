@@ -33,7 +33,24 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kQueries = 32 * kWaves;
 constexpr int kKeys = 64;  // of a tile
-constexpr float kSlack = 8.0f;
+// A score may pass the running maximum by 2^SLACK before everything is rescaled; probabilities are
+// taken times 2^SHIFT.  In binary16 together 2^15, all that the type has room for: it keeps its 11
+// bits of a probability down to 2^-25 of the largest (17 nats) and holds them down to 2^-36.  (With 2^8
+// and 2^0, keys 16 nats below a heavy one whose values are 0 were off by 9 times the half unit.  The smaller slack
+// costs nothing at scores of width 1 and 1.6 % at width 3: 8192 tokens 675 and 696 us.)
+template <typename T>
+struct Range {
+  static constexpr float SLACK = 8.0f, SHIFT = 0.0f;
+};
+template <>
+struct Range<_Float16> {
+  static constexpr float SLACK = 4.0f, SHIFT = 11.0f;
+};
+// What is taken from a score (base 2) with the running maximum m
+template <typename T>
+__device__ __forceinline__ float score_base(float m) {
+  return (m == -__builtin_inff() ? 0.0f : m) - Range<T>::SHIFT;
+}
 
 struct PromptArgs {
   const uint16_t *q, *k, *v;
@@ -123,13 +140,13 @@ struct Stage {
 };
 
 // Query `row_q` of a head by itself, out of memory and on the vector unit, for its keys 0 .. limit:
-// lanes take keys for the scores, pairs of channels for the result.  `m`: a maximum within
-// 2^kSlack.  Its tiles reached to row `last` of the values: nothing is done if no channel has
-// a value that is not finite behind `limit`, or if a NaN among the last 64 rows up to it makes the
-// same NaN of the channel (as where a channel is NaN in every row).  2048 tokens (40/8 heads of 128):
+// lanes take keys for the scores, pairs of channels for the result.  `base`: what is taken from the
+// scores (score_base).  Its tiles reached to row `last` of the values: nothing is done if no
+// channel has a value that is not finite behind `limit`, or if a NaN among the last 64 rows up to it
+// makes the same NaN of the channel (as where a channel is NaN in every row).  2048 tokens (40/8 heads of 128):
 // 0.44 ms with NaN in every value, 4.5 with one such row, 10 with an infinite channel.
 template <typename T, int NB>
-__device__ __forceinline__ void one_query(const PromptArgs& a, const Span& sp, int head, int kvh, int row_q, int limit, int last, float m) {
+__device__ __forceinline__ void one_query(const PromptArgs& a, const Span& sp, int head, int kvh, int row_q, int limit, int last, float base) {
   const int lane = (int)(threadIdx.x & 63);
   constexpr int SETS = (NB + 3) / 4;  // pairs 64 x + lane
   const auto value_pair = [&](int j, int x, float (&y)[2]) __attribute__((always_inline)) {
@@ -172,7 +189,7 @@ __device__ __forceinline__ void one_query(const PromptArgs& a, const Span& sp, i
         }
       }
       float t[2];  // (rounded to the operand type as everywhere)
-      unpack_pair<T>(pack_pair<T>(exp2_fast(__builtin_fmaf(s, a.scale_log2, -m)), 0.0f), t);
+      unpack_pair<T>(pack_pair<T>(exp2_fast(__builtin_fmaf(s, a.scale_log2, -base)), 0.0f), t);
       p = t[0];
     }
     const int some = min(64, limit - j0 + 1);
@@ -316,7 +333,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
   // Tile t in `slot`: its probabilities and their product with the values, and the next tile's
   // scores, which depend on neither
   const auto step = [&](int t, int slot, floatx16 (&s)[2], floatx16 (&next)[2]) __attribute__((always_inline)) {
-    if (__any(top > m + kSlack)) {
+    if (__any(top > m + Range<T>::SLACK)) {
       const float m_new = fmaxf(m, max_32(top));
       const float f = m_new == -__builtin_inff() ? 1.0f : exp2_fast(m - m_new);
       l *= f;
@@ -331,7 +348,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
       else
         buffer_to_lds(keys, key_from[j - S::LOADS], keys_at + slot * S::BYTES + 1024 * (j - S::LOADS));
     });
-    const float m_safe = m == -__builtin_inff() ? 0.0f : m;
+    const float base = score_base<T>(m);
     Frag pf[2][2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
@@ -339,8 +356,8 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float x = exp2_fast(__builtin_fmaf(s[kb][8 * h + 2 * j], a.scale_log2, -m_safe));
-          const float y = exp2_fast(__builtin_fmaf(s[kb][8 * h + 2 * j + 1], a.scale_log2, -m_safe));
+          const float x = exp2_fast(__builtin_fmaf(s[kb][8 * h + 2 * j], a.scale_log2, -base));
+          const float y = exp2_fast(__builtin_fmaf(s[kb][8 * h + 2 * j + 1], a.scale_log2, -base));
           pf[kb][h].v[j] = pack_pair<T>(x, y);
           l = add_pair<T>(pf[kb][h].v[j], l);
         }
@@ -422,7 +439,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
   for (; again; again &= again - 1) {
     const int x = __builtin_ctz(again);
     const float m_x = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, m), x));
-    one_query<T, NB>(a, sp, head, kvh, sp.q0 + iw + x, min(iw + x + shift, sp.n - 1), min(sp.n, mine * kKeys) - 1, m_x == -__builtin_inff() ? 0.0f : m_x);
+    one_query<T, NB>(a, sp, head, kvh, sp.q0 + iw + x, min(iw + x + shift, sp.n - 1), min(sp.n, mine * kKeys) - 1, score_base<T>(m_x));
   }
 }
 

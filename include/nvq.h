@@ -524,7 +524,8 @@ nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b,
  * Hq a multiple of Hkv; Tq, Tk < 2^30; token strides of k and v below 2^24 elements.  Rows of
  * out in no sequence are left alone; offsets outside the tensors are cut to them.  Scores,
  * softmax statistics and accumulation are float32; the probabilities enter the second product
- * rounded once to `type`.  Keys and values that a query does not see never matter, whatever they
+ * rounded once to `type` (in binary16 to its 11 bits down to 2^-25 of the largest, with fewer down
+ * to 2^-36, below that as 0).  Keys and values that a query does not see never matter, whatever they
  * hold (queries that an infinity or NaN in such a value row of their tile would reach are done
  * one by one, slowly).  out overlaps none of the inputs. */
 nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v, void* out,

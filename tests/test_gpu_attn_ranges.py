@@ -4,8 +4,9 @@ every other test: each probability to the rounding that its operator states, wha
 import numpy as np
 import pytest
 
-from attn_cases import Paged, attention, bound, check
+from attn_cases import HALF_UNIT, Paged, attention, bound, check, rounded
 from gpu_cases import host, say, torch_dev
+from test_gpu_attn_prompt import call, on_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +65,28 @@ def test_decode_values_near_the_top_of_bfloat16():
     k[:128, :, 0] = 0.0
     v = (r.uniform(0.5, 0.99, (n, Hkv, D)) * 2.0 ** 114).astype(np.float32)
     decode("bf16", [(k, v)], queries(r, 1, Hkv, D), D, 64, 5, "large values", (0, 17, 63))
+
+
+def prompt(q, k, v, type_, D, what):
+    m, n = len(q), len(k)
+    cu = [np.array([0, x], np.int32) for x in (m, n)]
+    got = host(call(*(on_gpu(x, type_) for x in (q, k, v)), *cu, scale=1.0).float())
+    seen = np.arange(n)[None] <= np.arange(m)[:, None] + (n - m)
+    worst = 0.0
+    for h in range(q.shape[1]):
+        want, A, S = attention(q[:, h], k[:, 0], v[:, 0], 1.0, seen)
+        worst = max(worst, check(got[:, h], want, bound(want, A, S, D, n, type_, HALF_UNIT[type_], 2), f"{what} head {h}"))
+    say(f"  worst error / bound {worst:.3g}")
+
+
+@pytest.mark.parametrize("type_,gap", [("f16", 8), ("f16", 11), ("f16", 14), ("f16", 16), ("bf16", 16), ("bf16", 30), ("bf16", 60)])
+def test_prompt_small_probabilities(type_, gap):
+    """The heavy key is the first one, so every query sees it; probabilities down to e^-17 of the largest (binary16)."""
+    say(f"prompt small probabilities {type_} gap={gap}")
+    r = np.random.Generator(np.random.PCG64(gap))
+    D, m, n = 64, 70, 2100
+    k, v = (rounded(x, type_) for x in far_rows(r, n, 1, D, 0, gap))
+    q = rounded(queries(r, m, 2, D) * np.where(np.arange(D) == 0, 1.0, 0.3).astype(np.float32), type_)
+    s = q[:, :, 1:].reshape(-1, D - 1) @ k[:, 0, 1:].T
+    assert np.abs(s).max() < 1.0  # so that all probabilities lie within a nat of e^-gap
+    prompt(q, k, v, type_, D, f"{type_} gap {gap}")
