@@ -34,13 +34,14 @@ constexpr int kWaves = 4;
 constexpr int kQueries = 32 * kWaves;
 constexpr int kKeys = 64;  // of a tile
 // A score may pass the running maximum by 2^SLACK before everything is rescaled; probabilities are
-// taken times 2^SHIFT.  In binary16 together 2^15, all that the type has room for: it keeps its 11
+// taken times 2^SHIFT.  In bfloat16 they are at most 1 with it: values reach to the top of float32, and
+// times 2^SLACK they would pass it where the result does not.  In binary16 together 2^15, all that the type has room for: it keeps its 11
 // bits of a probability down to 2^-25 of the largest (17 nats) and holds them down to 2^-36.  (With 2^8
 // and 2^0, keys 16 nats below a heavy one whose values are 0 were off by 9 times the half unit.  The smaller slack
 // costs nothing at scores of width 1 and 1.6 % at width 3: 8192 tokens 675 and 696 us.)
 template <typename T>
 struct Range {
-  static constexpr float SLACK = 8.0f, SHIFT = 0.0f;
+  static constexpr float SLACK = 8.0f, SHIFT = -8.0f;
 };
 template <>
 struct Range<_Float16> {

@@ -90,3 +90,15 @@ def test_prompt_small_probabilities(type_, gap):
     s = q[:, :, 1:].reshape(-1, D - 1) @ k[:, 0, 1:].T
     assert np.abs(s).max() < 1.0  # so that all probabilities lie within a nat of e^-gap
     prompt(q, k, v, type_, D, f"{type_} gap {gap}")
+
+
+def test_prompt_values_near_the_top_of_bfloat16():
+    say("prompt values of 2^113 .. 2^114")
+    r = np.random.Generator(np.random.PCG64(6))
+    D, m, n = 64, 40, 4000
+    k = (r.standard_normal((n, 1, D)) * 2.0 ** -6).astype(np.float32)
+    k[:, :, 0] = 5.375
+    k[:64, :, 0] = 0.0
+    k = rounded(k, "bf16")
+    v = rounded(r.uniform(0.5, 0.99, (n, 1, D)) * 2.0 ** 114, "bf16")
+    prompt(rounded(queries(r, m, 2, D), "bf16"), k, v, "bf16", D, "large values")
