@@ -243,23 +243,30 @@ void launch_type(const KvArgs& a, int fmt, int nb, bool write, hipStream_t s) {
 hipError_t launch_kv_copy(bool write, int fmt, int type, const void* k, const void* v, const int64_t strides[4],
                           const int64_t* slots, int64_t T, int64_t heads, int64_t D, const KvCache& c, hipStream_t stream) {
   KvArgs a;
-  a.rows[0] = k, a.rows[1] = v;
   a.stride_t[0] = strides[0], a.stride_h[0] = strides[1], a.stride_t[1] = strides[2], a.stride_h[1] = strides[3];
   a.codes[0] = (uint8_t*)c.k, a.codes[1] = (uint8_t*)c.v;
   a.scales[0] = (uint16_t*)c.k_d, a.scales[1] = (uint16_t*)c.v_d;
-  a.slots = slots;
-  a.n_rows = (int)(T * heads);
   a.n_slots = c.n_pages << c.page_shift;
   a.heads = (uint32_t)heads;
   a.page_shift = (uint32_t)c.page_shift;
   const int nb = (int)(D / 32);
-  if (type == NVQ_TYPE_F32)
-    launch_type<float>(a, fmt, nb, write, stream);
-  else if (type == NVQ_TYPE_F16)
-    launch_type<_Float16>(a, fmt, nb, write, stream);
-  else
-    launch_type<__bf16>(a, fmt, nb, write, stream);
-  return hipGetLastError();
+  // a launch takes fewer than 2^32 threads, 16 to a row: longer calls go in pieces
+  const int64_t most = ((int64_t(1) << 28) - 16) / heads;
+  for (int64_t t = 0; t < T; t += most) {
+    a.n_rows = (int)((T - t < most ? T - t : most) * heads);
+    for (int w = 0; w < 2; ++w)
+      a.rows[w] = (const char*)(w ? v : k) + t * a.stride_t[w] * (type == NVQ_TYPE_F32 ? 4 : 2);
+    a.slots = slots + t;
+    if (type == NVQ_TYPE_F32)
+      launch_type<float>(a, fmt, nb, write, stream);
+    else if (type == NVQ_TYPE_F16)
+      launch_type<_Float16>(a, fmt, nb, write, stream);
+    else
+      launch_type<__bf16>(a, fmt, nb, write, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace nvq
