@@ -784,9 +784,10 @@ size_t attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int6
   return (size_t)groups * ((size_t)(D / 16) * 64 * 16 + 2 * 16 * 4);
 }
 
-int64_t attn_decode_groups(int64_t B, int64_t Hq, int64_t Hkv, int64_t capacity) {
-  const int64_t G = Hq / Hkv;
-  return chunk_bound(B, Hkv, G, capacity) * Hkv * head_tiles(G);
+bool attn_decode_fits(int64_t B, int64_t Hq, int64_t Hkv, int64_t capacity) {
+  constexpr int64_t most = int64_t(1) << 32;
+  const int64_t per = Hkv * head_tiles(Hq / Hkv);
+  return chunk_bound(B, Hkv, Hq / Hkv, capacity) * per * 256 < most && (capacity <= kMinChunk || B * per * (64 * kJoinWaves) < most);
 }
 
 hipError_t launch_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b, int64_t q_stride_h, int64_t B,
@@ -802,7 +803,7 @@ hipError_t launch_attn_decode(int fmt, int type, const void* q, int64_t q_stride
   a.table_stride = (int)table_stride;
   a.target = (int)chunk_target(Hkv, a.G);
   const int64_t capacity = table_stride << c.page_shift;
-  const int64_t groups = attn_decode_groups(B, Hq, Hkv, capacity);
+  const int64_t groups = chunk_bound(B, Hkv, a.G, capacity) * Hkv * a.HT;
   a.acc = (float*)workspace;
   a.stat = a.acc + groups * (D / 16) * 64 * 4;
   const bool join = capacity > kMinChunk;

@@ -25,10 +25,10 @@
 
 namespace nvq {
 
-// Every query tile of every head; a multiple of the chip's parts (find_place).
-int64_t attn_prompt_groups(int64_t B, int64_t Tq, int64_t Hq) { return ((Tq / 128 + B) * Hq + 7) / 8 * 8; }
-
 namespace {
+
+// Every query tile of every head; a multiple of the chip's parts (find_place).
+int64_t prompt_groups(int64_t B, int64_t Tq, int64_t Hq) { return ((Tq / 128 + B) * Hq + 7) / 8 * 8; }
 
 constexpr int kWaves = 4;
 constexpr int kQueries = 32 * kWaves;
@@ -446,7 +446,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_prompt_kern
 
 template <typename T, int NB>
 hipError_t launch_nb(const PromptArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((attn_prompt_kernel<T, NB>), dim3((unsigned)attn_prompt_groups(a.B, a.Tq, a.Hq)), dim3(64 * kWaves), 0, s, a);
+  hipLaunchKernelGGL((attn_prompt_kernel<T, NB>), dim3((unsigned)prompt_groups(a.B, a.Tq, a.Hq)), dim3(64 * kWaves), 0, s, a);
   return hipGetLastError();
 }
 template <typename T>
@@ -464,6 +464,8 @@ hipError_t launch_type(const PromptArgs& a, int nb, hipStream_t s) {
 }
 
 }  // namespace
+
+bool attn_prompt_fits(int64_t B, int64_t Tq, int64_t Hq) { return prompt_groups(B, Tq, Hq) * (64 * kWaves) < int64_t(1) << 32; }
 
 hipError_t launch_attn_prompt(int type, const void* q, const void* k, const void* v, void* out, const int64_t strides[8],
                               const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,

@@ -719,7 +719,7 @@ nvq_status nvq_kv_read(int fmt, int type, void* k, int64_t k_stride_t, int64_t k
 static bool decode_shape_ok(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages, int64_t page) {
   return B >= 1 && B < kMaxDim && Hkv >= 1 && Hkv <= 65536 && Hq >= Hkv && Hq <= 65536 && Hq % Hkv == 0 && D >= 32 && D <= 256 &&
          D % 32 == 0 && page_ok(page) && max_pages >= 1 && max_pages < kMaxDim / 2 / page && B * (max_pages * page) < kMaxDim / 2 &&
-         nvq::attn_decode_groups(B, Hq, Hkv, max_pages * page) < kMaxDim;
+         nvq::attn_decode_fits(B, Hq, Hkv, max_pages * page);
 }
 
 size_t nvq_attn_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages, int64_t page) {
@@ -737,7 +737,7 @@ nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b,
   NVQ_TRY(check_cache(who, fmt, k_cache, v_cache, k_d, v_d, Hkv, D, n_pages, page, c));
   if (B == 0) return NVQ_OK;
   if (!decode_shape_ok(B, Hq, Hkv, D, max_pages, page))
-    return fail(NVQ_ERR_SHAPE, "%s: B=%lld, Hq=%lld, Hkv=%lld, max_pages=%lld, page=%lld out of range (Hq a multiple of Hkv, B * max_pages * page < 2^30)",
+    return fail(NVQ_ERR_SHAPE, "%s: B=%lld, Hq=%lld, Hkv=%lld, max_pages=%lld, page=%lld out of range (Hq a multiple of Hkv, B * max_pages * page < 2^30, B * Hkv * ceil(Hq / Hkv / 16) < 2^23)",
                 who, (long long)B, (long long)Hq, (long long)Hkv, (long long)max_pages, (long long)page);
   if (!q || !table || !lengths || !out) return fail(NVQ_ERR_NULL, "%s: NULL pointer", who);
   NVQ_TRY(check_rows(who, "q", q, type, B, Hq, q_stride_b, q_stride_h));
@@ -771,8 +771,9 @@ nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v
   // a tile's 64 rows are addressed by 32-bit offsets
   if (Tk > 1 && (strides[2] >= (int64_t(1) << 24) || strides[4] >= (int64_t(1) << 24)))
     return fail(NVQ_ERR_SHAPE, "%s: token strides of k and v must be below 2^24 elements", who);
+  if (!nvq::attn_prompt_fits(B, Tq, Hq))
+    return fail(NVQ_ERR_SHAPE, "%s: B=%lld, Tq=%lld: too many query tiles ((Tq / 128 + B) * Hq < 2^24)", who, (long long)B, (long long)Tq);
   if (!aligned(cu_q, 4) || !aligned(cu_k, 4)) return fail(NVQ_ERR_ALIGN, "%s: cu_q and cu_k must be 4-byte aligned", who);
-  if (nvq::attn_prompt_groups(B, Tq, Hq) >= kMaxDim) return fail(NVQ_ERR_SHAPE, "%s: too many query tiles", who);
   NVQ_TRY(check_device());
   return launched(nvq::launch_attn_prompt(type, q, k, v, out, strides, cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, scale, causal ? 1 : 0,
                                           (hipStream_t)stream), who);

@@ -119,20 +119,22 @@ struct KvCache {
 // head stride, v's, in elements.
 hipError_t launch_kv_copy(bool write, int fmt, int type, const void* k, const void* v, const int64_t strides[4],
                           const int64_t* slots, int64_t T, int64_t heads, int64_t D, const KvCache& c, hipStream_t stream);
-// Attention of one token per sequence over the cache (attn_decode.hip); groups: its workgroups.
+// Attention of one token per sequence over the cache (attn_decode.hip).
 hipError_t launch_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b, int64_t q_stride_h, int64_t B,
                               int64_t Hq, int64_t Hkv, int64_t D, const KvCache& c, const int32_t* table,
                               int64_t table_stride, const int32_t* lengths, float scale, void* out, void* workspace,
                               hipStream_t stream);
 size_t attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity);
-int64_t attn_decode_groups(int64_t B, int64_t Hq, int64_t Hkv, int64_t capacity);
+// Whether its launches (and prompt attention's) stay below 2^32 threads: a longer one would be cut short
+// without an error.
+bool attn_decode_fits(int64_t B, int64_t Hq, int64_t Hkv, int64_t capacity);
+bool attn_prompt_fits(int64_t B, int64_t Tq, int64_t Hq);
 
 // Attention of packed prompts (attn_prompt.hip); strides: token and head stride of q, k, v
-// and out, in elements; groups: its workgroups.
+// and out, in elements.
 hipError_t launch_attn_prompt(int type, const void* q, const void* k, const void* v, void* out, const int64_t strides[8],
                               const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,
                               int64_t Hkv, int64_t D, float scale, int causal, hipStream_t stream);
-int64_t attn_prompt_groups(int64_t B, int64_t Tq, int64_t Hq);
 
 // Measurement probes (probe.hip): a streaming read of n16 16-byte units over `blocks`
 // blocks of 256 threads (sink: 4 words per block); the decode GEMV's weight loads

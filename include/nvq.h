@@ -498,7 +498,8 @@ nvq_status nvq_kv_read(int fmt, int type, void* k, int64_t k_stride_t, int64_t k
  * with k_j, v_j the cache rows of key head h / (Hq/Hkv) at place j of sequence b: page
  * table[b][j / page], place j % page.  q [B][Hq][D] of `type` (strides between sequences and
  * between heads), out [B][Hq][D] of `type`, contiguous; table int32 [B][max_pages] and lengths
- * int32 [B] on the device.  Hq a multiple of Hkv; B * max_pages * page < 2^30.  A sequence
+ * int32 [B] on the device.  Hq a multiple of Hkv; B * max_pages * page < 2^30;
+ * B * Hkv * ceil(Hq/Hkv/16) < 2^23 (2^24 where max_pages * page <= 128).  A sequence
  * of length 0 gives zeros; a length outside 0 .. max_pages * page, or a page number outside the
  * cache among its keys, gives NaN (nothing is read there).  Scores, sums and products are as
  * exact as float32 makes them (two binary16 terms, or three bfloat16 terms, of each float
@@ -521,7 +522,7 @@ nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b,
  * keys, query i sees keys j <= i + n - m if causal (the last query sees all: n > m puts the
  * queries behind n - m keys of a prefix), else all n.  A query that sees no key gives zeros.
  * `type` NVQ_TYPE_F16 or BF16; strides[8]: token and head stride of q, k, v and out (host).
- * Hq a multiple of Hkv; Tq, Tk < 2^30; token strides of k and v below 2^24 elements.  Rows of
+ * Hq a multiple of Hkv; Tq, Tk < 2^30, (Tq/128 + B) * Hq < 2^24; token strides of k and v below 2^24 elements.  Rows of
  * out in no sequence are left alone; offsets outside the tensors are cut to them.  Scores,
  * softmax statistics and accumulation are float32; the probabilities enter the second product
  * rounded once to `type` (in binary16 to its 11 bits down to 2^-25 of the largest, with fewer down

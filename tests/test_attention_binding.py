@@ -94,3 +94,20 @@ def test_scratch_comes_from_the_stream_that_uses_it(monkeypatch, stream, want):
     assert nvq._workspace(4096, stream, types.SimpleNamespace(device="cuda:0")) is not None
     assert asked == [(4096, want, "cuda:0")] and current == [77]
     assert nvq._workspace(0, stream, None) is None
+
+
+def test_calls_of_more_threads_than_a_launch_takes_are_refused():
+    """A launch takes fewer than 2^32 threads (256 to a workgroup, 512 to one that joins parts); a longer one is cut short
+    without an error, so the entries refuse what would need it."""
+    from test_attention_host import ALIGN, NULL, SHAPE, P, decode, prompt
+
+    ws = nvq.nvq_attn_decode_workspace_bytes
+    # 128 keys at most: no parts to join
+    assert decode(B=1 << 21, max_pages=2, q=None) == SHAPE and decode(B=(1 << 21) - 1, max_pages=2, q=None) == NULL
+    assert decode(B=1 << 20, Hq=8 * 17, max_pages=2, q=None) == SHAPE and decode(B=(1 << 20) - 1, Hq=8 * 17, max_pages=2, q=None) == NULL
+    # 256 keys: parts
+    assert decode(B=1 << 20, max_pages=4, q=None) == SHAPE and ws(1 << 20, 40, 8, 128, 4, 64) == 0
+    assert decode(B=(1 << 20) - 1, max_pages=4, q=None) == NULL and ws((1 << 20) - 1, 40, 8, 128, 4, 64) > 0
+    assert prompt(B=1 << 19, Hq=32, cu_q=P + 2) == SHAPE and "query tiles" in nvq.last_error()
+    assert prompt(B=1, Tq=1 << 29, Hq=8, cu_q=P + 2) == SHAPE
+    assert prompt(B=(1 << 19) - 1, Hq=32, cu_q=P + 2) == ALIGN
