@@ -31,6 +31,7 @@ class AttentionLayer:
         self.w_qkv, self.s_qkv, self.qkv_logical = self._weights(self.rows, hidden, seed + 1)
         self.w_o, self.s_o, self.o_logical = self._weights(hidden, heads * head_dim, seed + 2)
         pages = -(-max_tokens // page)
+        self.max_tokens = pages * page
         shape = (pages, kv_heads, page, head_dim)
         self.codes = [torch.zeros(shape, dtype=torch.int8, device="cuda") for _ in "kv"]
         self.scales = [torch.zeros((*shape[:3], head_dim // 32), dtype=torch.float16, device="cuda") for _ in "kv"]
@@ -49,6 +50,10 @@ class AttentionLayer:
         y = self._product(w, 1.0, torch.from_numpy(synth.activations(8, K, seed)).cuda(), N)
         s = float(np.float32(1.0 / float(y.square().mean().sqrt())))
         return w, s, (codes, scales, s)
+
+    def _room(self, count):
+        if count < 1 or self.n + count > self.max_tokens:
+            raise ValueError("%d tokens behind %d: the cache takes 1 to %d more" % (count, self.n, self.max_tokens - self.n))
 
     def _slots(self, first, count):
         at = torch.arange(first, first + count, device="cuda")
@@ -72,6 +77,7 @@ class AttentionLayer:
     def prompt(self, x):
         """x [M, hidden] float32, the next M tokens: [M, hidden].  What is already in the cache is read back."""
         M, prefix = x.shape[0], self.n
+        self._room(M)
         q, k, v = self._split(self._product(self.w_qkv, self.s_qkv, x, self.rows))
         nvq.nvq_kv_write(k, v, self._slots(prefix, M), *self.codes, *self.scales)
         keys, values = (torch.empty((prefix + M, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device="cuda") for _ in "kv")
@@ -86,6 +92,7 @@ class AttentionLayer:
 
     def step(self, x):
         """x [1, hidden] float32, the next token: [1, hidden]."""
+        self._room(1)
         y = torch.empty((1, self.rows), dtype=torch.float32, device="cuda")
         nvq.nvq_gemv_nvfp4_fused(self.w_qkv, self.s_qkv, x, y)
         q, k, v = self._split(y)
@@ -108,6 +115,8 @@ def main():
     p.add_argument("--kv-heads", type=int, default=8)
     p.add_argument("--head-dim", type=int, default=128)
     a = p.parse_args()
+    if a.prompt < 2 or a.steps < 1:
+        p.error("a prompt of two tokens or more (it goes in two pieces) and a step or more")
     layer = AttentionLayer(a.hidden, a.heads, a.kv_heads, a.head_dim, a.prompt + a.steps + 1)
     x = torch.from_numpy(synth.activations(a.prompt + a.steps, a.hidden, 3)).cuda()
     half = a.prompt // 2
