@@ -780,7 +780,7 @@ def nvq_attn_decode(q, k_cache, v_cache, table, lengths, out, k_d=None, v_d=None
     wp, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = L.nvq_attn_decode(fmt, code, q.data_ptr(), qs[0], qs[1], B, Hq, heads, D, k_cache.data_ptr(), v_cache.data_ptr(),
                            None if fmt else k_d.data_ptr(), None if fmt else v_d.data_ptr(), n_pages, page, table.data_ptr(), max_pages,
-                           lengths.data_ptr(), D ** -0.5 if scale is None else scale, out.data_ptr(), wp, ws_bytes,
+                           lengths.data_ptr(), max(D, 1) ** -0.5 if scale is None else scale, out.data_ptr(), wp, ws_bytes,
                            _torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream))
     if st:
         _check(st, "nvq_attn_decode")
@@ -819,7 +819,7 @@ def nvq_attn_prompt(q, k, v, cu_q, cu_k, out, scale=None, causal=True, stream=No
         raise ValueError("q, k, v, out, cu_q and cu_k do not fit together")
     strides = _Strides(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], ps[0], ps[1])
     st = L.nvq_attn_prompt(_row_types[dtype], q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), strides, cu_q.data_ptr(), cu_k.data_ptr(),
-                           n[0] - 1, Tq, Tk, Hq, Hkv, D, D ** -0.5 if scale is None else scale, 1 if causal else 0,
+                           n[0] - 1, Tq, Tk, Hq, Hkv, D, max(D, 1) ** -0.5 if scale is None else scale, 1 if causal else 0,
                            _torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream))
     if st:
         _check(st, "nvq_attn_prompt")

@@ -111,3 +111,17 @@ def test_calls_of_more_threads_than_a_launch_takes_are_refused():
     assert prompt(B=1 << 19, Hq=32, cu_q=P + 2) == SHAPE and "query tiles" in nvq.last_error()
     assert prompt(B=1, Tq=1 << 29, Hq=8, cu_q=P + 2) == SHAPE
     assert prompt(B=(1 << 19) - 1, Hq=32, cu_q=P + 2) == ALIGN
+
+
+def test_a_width_of_zero_is_the_librarys_refusal(monkeypatch):
+    """(Not a division by zero in the default scale.)"""
+    import torch
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # CPU tensors' own
+    q, c, d = torch.zeros((1, 2, 0)), torch.zeros((2, 1, 16, 0), dtype=torch.int8), torch.zeros((2, 1, 16, 0), dtype=torch.float16)
+    t, n = torch.zeros((1, 2), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    h, cu = torch.zeros((4, 2, 0), dtype=torch.float16), torch.tensor([0, 4], dtype=torch.int32)
+    for call in (lambda: nvq.nvq_attn_decode(q, c, c, t, n, q, d, d, stream=0), lambda: nvq.nvq_attn_prompt(h, h, h, cu, cu, h, stream=0)):
+        with pytest.raises(nvq.NvqError) as e:
+            call()
+        assert e.value.status == -2
