@@ -474,6 +474,8 @@ hipError_t launch_attn_prompt(int type, const void* q, const void* k, const void
   a.q = (const uint16_t*)q, a.k = (const uint16_t*)k, a.v = (const uint16_t*)v, a.out = (uint16_t*)out;
   a.q_t = strides[0], a.q_h = strides[1], a.k_t = strides[2], a.k_h = strides[3];
   a.v_t = strides[4], a.v_h = strides[5], a.o_t = strides[6], a.o_h = strides[7];
+  // the token stride of a single row, which has no meaning, tells the kernel where rows end
+  if (Tk <= 1) a.k_t = a.v_t = D;
   a.cu_q = cu_q, a.cu_k = cu_k;
   a.B = (int)B, a.Hq = (int)Hq, a.Hkv = (int)Hkv, a.G = (int)(Hq / Hkv), a.Tq = (int)Tq, a.Tk = (int)Tk;
   // a negative scale turns the queries round, so that the largest score is the largest product
