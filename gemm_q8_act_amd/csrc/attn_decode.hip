@@ -39,10 +39,14 @@ namespace {
 
 constexpr int kTile = 32;          // keys of one wavefront's step
 // The shortest chunk is one tile to a wavefront: 500 keys of 8 key heads in chunks of 128 take
-// 10.8 us, in chunks of 256 12.2 (a tile's latency, 1.8 us, against the wait for one more part).
+// 10.2 us, in chunks of 256 11.6 (a tile's latency, 1.8 us, against the wait for one more part).
 constexpr int kMinChunk = 128;  // keys
-// Two workgroups to a compute unit, all at once: 131071 keys 64 us, with 1024 71 (8 ragged
-// sequences of up to 4096: 19 and 24).
+// Two workgroups to each of 256 compute units.  LDS holds that many at once, or more, over Q8_0 up
+// to 128 channels and in 16 bits up to 64; from 160 channels in Q8_0 and 96 in 16 bits it holds one,
+// and the second half waits.  Q8_0, 128 channels: 131071 keys 59 us, with 256 the same, with 1024 63 (8 ragged
+// sequences of up to 4096: 17.6, 18.1 and 23).  No one number is best where one workgroup fits: binary16, 8 x 4096
+// keys, 4 heads of 256: 44 us, with 256 34; bfloat16, 64 ragged sequences of 128 channels: 190 at either, with
+// 1024 186.
 constexpr int kTargetGroups = 512;
 constexpr int kJoinWaves = 8;
 // A score may pass the running maximum by 2^kSlack before everything is rescaled.
@@ -167,8 +171,9 @@ struct Shape {
   static constexpr int SLOT = 4 * GROUP + 4 * SCALES;
   // Two tiles' room a wavefront.  Rows wider than 256 bytes leave room for two wavefronts.
   static constexpr int WAVES = 2 * 4 * SLOT <= 144 * 1024 ? 4 : 2;
-  // Wavefronts of a SIMD that the registers are cut for: two, so that the accumulator stays in
-  // ordinary registers (with one it moves to the other half and back in every step), where it all fits.
+  // Wavefronts of a SIMD that the registers are cut for: two (also where LDS leaves room for one), so that
+  // the accumulator stays in ordinary registers (with one it moves to the other half and back in
+  // every step), where it all fits.
   static constexpr int EU_WAVES = NB <= (Q8 ? 4 : 5) ? 2 : 1;
   // 16-byte pieces of a key row, and which row bits they are exchanged by in LDS, so that the
   // lanes of one piece of different rows fall on different banks (64 of 4 bytes)

@@ -11,9 +11,15 @@
 // the softmax into the product without leaving their registers.  V^T's operands are read from
 // the row-major tile by the transposing LDS read (ds_read_b64_tr_b16).
 //
+// Probabilities enter the second product rounded once to the operands' type, as the sum that divides it
+// takes them; scores, statistics and accumulators are float32.  That rounding is as large as the
+// result's own and makes errors 1.1 to 1.4 times those of a float32 form.  Two terms would double the
+// second product, half of the work.
+//
 // What bounds it: issue.  A wavefront's 64-key step is 8 D/32 products of 32 cycles, each beside
 // one exponential and about 4 other vector instructions (128 channels): 8192 tokens of
-// 40 heads of 128 over 8 key heads take 609 us, 1120 TFLOP/s, the matrix cores busy 59 % of it.
+// 40 heads of 128 over 8 key heads take 610 to 640 us by the card, up to 1120 TFLOP/s, the matrix cores busy
+// 59 % of it.
 // So a step's vector work (the softmax of tile t) stands beside products that do not depend on it
 // (the scores of tile t + 1), two wavefronts share a SIMD, and tiles come straight into LDS, which is
 // read for one product at a time.  32 queries a wavefront, since 64 do not fit the registers
@@ -144,8 +150,9 @@ struct Stage {
 // lanes take keys for the scores, pairs of channels for the result.  `base`: what is taken from the
 // scores (score_base).  Its tiles reached to row `last` of the values: nothing is done if no
 // channel has a value that is not finite behind `limit`, or if a NaN among the last 64 rows up to it
-// makes the same NaN of the channel (as where a channel is NaN in every row).  2048 tokens (40/8 heads of 128):
-// 0.44 ms with NaN in every value, 4.5 with one such row, 10 with an infinite channel.
+// makes the same NaN of the channel (as where a channel is NaN in every row).  A query costs all its keys
+// in one wavefront, so a call the square of its length.  40/8 heads of 128, 2048 tokens: 0.44 ms with NaN in every
+// value, 4.5 with one such row, 10 with an infinite channel, and at 8192 tokens 115.
 template <typename T, int NB>
 __device__ __forceinline__ void one_query(const PromptArgs& a, const Span& sp, int head, int kvh, int row_q, int limit, int last, float base) {
   const int lane = (int)(threadIdx.x & 63);
