@@ -36,6 +36,8 @@ NVQ_TYPE_BF16 = 2
 NVQ_KV_Q8_0 = 0
 NVQ_KV_F16 = 1
 NVQ_KV_BF16 = 2
+NVQ_ROPE_HALVES = 0
+NVQ_ROPE_NEIGHBOURS = 1
 
 # Every symbol include/nvq.h and include/nvq_probe.h declare.
 EXPORTS = (
@@ -49,6 +51,7 @@ EXPORTS = (
     "nvq_q5_k_weight_bytes", "nvq_q6_k_weight_bytes", "nvq_pack_q5_k", "nvq_pack_q6_k",
     "nvq_gemv_q5_k", "nvq_gemm_q5_k", "nvq_gemv_q6_k", "nvq_gemm_q6_k",
     "nvq_kv_write", "nvq_kv_read", "nvq_attn_decode_workspace_bytes", "nvq_attn_decode", "nvq_attn_prompt",
+    "nvq_rope_table", "nvq_qk_norm_rope", "nvq_rope_kv_write",
     "nvq_status_str", "nvq_last_error",
     "nvq_probe_read", "nvq_probe_gemv_loads", "nvq_probe_mfma",
 )
@@ -121,6 +124,11 @@ def lib() -> ctypes.CDLL:
                                                I64, I64, P, I64, P, F, P, P, SZ, P]),
             "nvq_attn_prompt": (ctypes.c_int, [ctypes.c_int, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, F,
                                                ctypes.c_int, P]),
+            "nvq_rope_table": (ctypes.c_int, [P, I64, I64, P]),
+            "nvq_qk_norm_rope": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, P, I64, I64, P, I64, I64, I64, I64, I64, I64, P, P, F, P, I64, I64,
+                                                ctypes.c_int, P, ctypes.c_int, P, P, I64, I64, P, I64, I64, P]),
+            "nvq_rope_kv_write": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, P, I64, I64, P, I64, I64, P, I64, I64, I64, I64, I64, I64,
+                                                 P, P, F, P, I64, I64, ctypes.c_int, P, ctypes.c_int, P, P, P, I64, I64, P, P, P, P, I64, I64, P]),
             "nvq_probe_read": (ctypes.c_int, [P, SZ, ctypes.c_int, P, P]),
             "nvq_probe_gemv_loads": (ctypes.c_int, [P, I64, I64, ctypes.c_int, ctypes.c_int, ctypes.c_int, P, P]),
             "nvq_probe_mfma": (ctypes.c_int, [ctypes.c_int, I64, ctypes.c_int, P, P]),
@@ -736,6 +744,171 @@ def nvq_kv_read(k_cache, v_cache, slots, k, v, k_d=None, v_d=None, stream=None) 
     """The cache rows at slots int64 [T] into k, v [T, Hkv, D] (arguments as nvq_kv_write's)."""
     L = _lib if _torch is not None else _attn_lib()
     _kv_copy(L.nvq_kv_read, "nvq_kv_read", k, v, slots, k_cache, v_cache, k_d, v_d, stream)
+
+
+def nvq_rope_table(P: int, R: int, base: float = 10000.0, inv_freq=None) -> np.ndarray:
+    """The position rotation's table, float32 [P, R] on the host: of base^(-2 c / R), or of inv_freq [R/2]."""
+    if inv_freq is None:
+        if R < 1 or not base > 0:
+            raise ValueError("nvq_rope_table: R and base must be positive")
+        inv_freq = float(base) ** (-np.arange(R // 2) * 2.0 / R)
+    inv_freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if inv_freq.shape != (R // 2,):
+        raise ValueError("inv_freq must be [R/2]")
+    out = np.empty((max(P, 0), max(R, 0)), np.float32)
+    _check(lib().nvq_rope_table(inv_freq.ctypes.data_as(ctypes.c_void_p), P, R, out.ctypes.data_as(ctypes.c_void_p)), "nvq_rope_table")
+    return out
+
+
+@functools.lru_cache(maxsize=64)
+def _sections(sections):
+    return (ctypes.c_int32 * len(sections))(*sections)
+
+
+_no_strides = (0, 0, 1)
+
+
+def _weight_fine(w, D):
+    return w is None or w.dtype is _torch.float32 and w.shape == (D,) and w.is_contiguous()
+
+
+def _rope_fine(table, positions, sections, T, q_weight, k_weight, D):
+    """Whether the table, the positions and the weights fit a call of T tokens; positions is [T] or [axes, T]."""
+    shape = positions.shape
+    axes = shape[0] if len(shape) == 2 else 1
+    return (shape[-1] == T and (len(shape) == 2 or len(shape) == 1) and positions.dtype is _torch.int32 and positions.is_contiguous()
+            and table.dtype is _torch.float32 and table.dim() == 2 and table.is_contiguous()
+            and (axes == 1 if sections is None else len(sections) == axes) and _weight_fine(q_weight, D) and _weight_fine(k_weight, D))
+
+
+def _rope_here(table, positions, q_weight, k_weight, here):
+    return (table.get_device() == here and positions.get_device() == here and (q_weight is None or q_weight.get_device() == here)
+            and (k_weight is None or k_weight.get_device() == here))
+
+
+def _wrong_rope(table, positions, sections, T, q_weight, k_weight, D):
+    if table is None or table.dim() != 2:
+        raise ValueError("table: float32 [positions, R] is required")
+    _wrong_dense(table, _torch.float32, table.shape, "table")
+    if positions is None or positions.dim() not in (1, 2):
+        raise ValueError("positions: int32 [T] or [axes, T] is required")
+    _wrong_dense(positions, _torch.int32, (*positions.shape[:-1], T), "positions")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if (axes != 1) if sections is None else len(sections) != axes:
+        raise ValueError("sections: a number of pairs for each axis of positions is required")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _wrong_dense(w, _torch.float32, (D,), name)
+
+
+def nvq_qk_norm_rope(q, k, table, positions, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, pairs=NVQ_ROPE_HALVES, sections=None,
+                     stream=None) -> None:
+    """Query and key heads [T, H, D] (strides free), normed (weights float32 [D]; None: not) and turned by the rows
+    of table float32 [P, R] at positions int32 [T], into q_out and k_out (strides free, one type, perhaps
+    another than q's).  q with q_out, or k with k_out, may be None.  Several axes: positions [axes, T], sections: pairs
+    of each."""
+    L = _lib if _torch is not None else _attn_lib()
+    here = -1
+    try:
+        x, o = (k, k_out) if q is None else (q, q_out)
+        T, _, D = x.shape
+        dtype, out_dtype = x.dtype, o.dtype
+        code, out_code = _row_types[dtype], _row_types[out_dtype]
+        qs, qo, Hq, ks, ko, Hkv = _no_strides, _no_strides, 1, _no_strides, _no_strides, 1
+        fine = _rope_fine(table, positions, sections, T, q_weight, k_weight, D)
+        if q is not None:
+            shape, qs, qo = q.shape, q.stride(), q_out.stride()
+            Hq = shape[1]
+            fine = (fine and shape == (T, Hq, D) and q.dtype is dtype and q_out.dtype is out_dtype and q_out.shape == shape and qs[2] == 1 and qo[2] == 1)
+        else:
+            fine = fine and q_out is None
+        if k is not None:
+            shape, ks, ko = k.shape, k.stride(), k_out.stride()
+            Hkv = shape[1]
+            fine = (fine and shape == (T, Hkv, D) and k.dtype is dtype and k_out.dtype is out_dtype and k_out.shape == shape and ks[2] == 1 and ko[2] == 1)
+        else:
+            fine = fine and k_out is None
+        if fine:
+            here = _torch.cuda.current_device()
+            fine = ((q is None or q.get_device() == here and q_out.get_device() == here) and (k is None or k.get_device() == here and k_out.get_device() == here)
+                    and _rope_here(table, positions, q_weight, k_weight, here))
+    except (AttributeError, KeyError, ValueError, IndexError, TypeError):
+        fine = False
+    if not fine:
+        if q is None and k is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
+            raise ValueError("q with q_out, k with k_out, or both are required")
+        x, o = (k, k_out) if q is None else (q, q_out)
+        _wrong_rows(x, x.dtype, x.shape, "k" if q is None else "q")
+        T, D = x.shape[0], x.shape[2]
+        for y, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+            if y is not None:
+                _wrong_rows(y, x.dtype, (T, y.shape[1] if y.dim() == 3 else -1, D), name)
+                _wrong_rows(out, o.dtype, y.shape, name + "_out")
+        _wrong_rope(table, positions, sections, T, q_weight, k_weight, D)
+        _wrong_device(q, k, table, positions, q_out, k_out, q_weight, k_weight)
+        raise ValueError("q, k, their outputs, table, positions and weights do not fit together")
+    st = L.nvq_qk_norm_rope(code, out_code, None if q is None else q.data_ptr(), qs[0], qs[1], None if k is None else k.data_ptr(), ks[0], ks[1], T, Hq,
+                            Hkv, D, None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps,
+                            table.data_ptr(), table.shape[0], table.shape[1], pairs, positions.data_ptr(), 1 if sections is None else len(sections),
+                            None if sections is None or len(sections) == 1 else _sections(tuple(sections)), None if q is None else q_out.data_ptr(),
+                            qo[0], qo[1], None if k is None else k_out.data_ptr(), ko[0], ko[1],
+                            _torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream))
+    if st:
+        _check(st, "nvq_qk_norm_rope")
+
+
+def nvq_rope_kv_write(q, k, v, table, positions, slots, q_out, k_cache, v_cache, k_d=None, v_d=None, q_weight=None, k_weight=None, eps=1e-6,
+                      pairs=NVQ_ROPE_HALVES, sections=None, stream=None) -> None:
+    """What a layer does with its QKV product, in one launch: keys [T, Hkv, D], normed and turned as nvq_qk_norm_rope's, and
+    values into a paged cache at slots as nvq_kv_write's; queries [T, Hq, D], normed and turned, into q_out (both
+    may be None)."""
+    L = _lib if _torch is not None else _attn_lib()
+    here = -1
+    try:
+        fmt, shape, rows, dtype = _cache_types[k_cache.dtype], k_cache.shape, k.shape, k.dtype
+        n_pages, heads, page, D = shape
+        T = rows[0]
+        ks, vs, code, out_code = k.stride(), v.stride(), _row_types[dtype], 0
+        qs, qo, Hq = _no_strides, _no_strides, 1
+        fine = (_cache_fine(fmt, shape, k_cache, v_cache, k_d, v_d) and rows == (T, heads, D) and v.shape == rows and v.dtype is dtype
+                and ks[2] == 1 and vs[2] == 1 and slots.dtype is _torch.int64 and slots.shape == rows[:1] and slots.is_contiguous()
+                and _rope_fine(table, positions, sections, T, q_weight, k_weight, D))
+        if q is not None:
+            shape, qs, qo, out_code = q.shape, q.stride(), q_out.stride(), _row_types[q_out.dtype]
+            Hq = shape[1]
+            fine = (fine and shape == (T, Hq, D) and q.dtype is dtype and q_out.shape == shape and qs[2] == 1 and qo[2] == 1)
+        else:
+            fine = fine and q_out is None
+        if fine:
+            here = _torch.cuda.current_device()
+            fine = (k.get_device() == here and v.get_device() == here and slots.get_device() == here and k_cache.get_device() == here
+                    and v_cache.get_device() == here and (fmt or k_d.get_device() == here and v_d.get_device() == here)
+                    and (q is None or q.get_device() == here and q_out.get_device() == here) and _rope_here(table, positions, q_weight, k_weight, here))
+    except (AttributeError, KeyError, ValueError, IndexError, TypeError):
+        fine = False
+    if not fine:
+        _wrong_cache(k_cache, v_cache, k_d, v_d)
+        T, (_, heads, _, D) = k.shape[0] if k is not None and k.dim() == 3 else -1, k_cache.shape
+        _wrong_rows(k, k.dtype if k is not None else None, (T, heads, D), "k")
+        _wrong_rows(v, k.dtype, (T, heads, D), "v")
+        _wrong_dense(slots, _torch.int64, (T,), "slots")
+        if (q is None) != (q_out is None):
+            raise ValueError("q and q_out are given together or not at all")
+        if q is not None:
+            _wrong_rows(q, k.dtype, (T, q.shape[1] if q.dim() == 3 else -1, D), "q")
+            _wrong_rows(q_out, q_out.dtype, q.shape, "q_out")
+        _wrong_rope(table, positions, sections, T, q_weight, k_weight, D)
+        _wrong_device(q, k, v, table, positions, slots, q_out, k_cache, v_cache, k_d, v_d, q_weight, k_weight)
+        raise ValueError("q, k, v, q_out, table, positions, slots, weights and the cache do not fit together")
+    st = L.nvq_rope_kv_write(fmt, code, out_code, None if q is None else q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                             T, Hq, heads, D, None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps,
+                             table.data_ptr(), table.shape[0], table.shape[1], pairs, positions.data_ptr(), 1 if sections is None else len(sections),
+                             None if sections is None or len(sections) == 1 else _sections(tuple(sections)), slots.data_ptr(),
+                             None if q is None else q_out.data_ptr(), qo[0], qo[1], k_cache.data_ptr(), v_cache.data_ptr(),
+                             None if fmt else k_d.data_ptr(), None if fmt else v_d.data_ptr(), n_pages, page,
+                             _torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream))
+    if st:
+        _check(st, "nvq_rope_kv_write")
 
 
 @functools.lru_cache(maxsize=256)  # a function of its arguments alone; a decode loop asks it each step

@@ -11,6 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -712,6 +713,117 @@ nvq_status nvq_kv_read(int fmt, int type, void* k, int64_t k_stride_t, int64_t k
                        void* stream) {
   return kv_copy(false, "nvq_kv_read", fmt, type, k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, slots, T, Hkv, D,
                  k_cache, v_cache, k_d, v_d, n_pages, page, stream);
+}
+
+nvq_status nvq_rope_table(const double* inv_freq, int64_t P, int64_t R, float* table) {
+  const char* who = "nvq_rope_table";
+  if (!inv_freq || !table) return fail(NVQ_ERR_NULL, "%s: NULL pointer", who);
+  if (R < 4 || R > 256 || R % 4 != 0) return fail(NVQ_ERR_SHAPE, "%s: R=%lld must be a multiple of 4 in 4 .. 256", who, (long long)R);
+  if (P < 1 || P >= kMaxDim) return fail(NVQ_ERR_SHAPE, "%s: P=%lld out of range", who, (long long)P);
+  for (int64_t p = 0; p < P; ++p)
+    for (int64_t c = 0; c < R / 2; ++c) {
+      const double angle = (double)p * inv_freq[c];
+      table[p * R + c] = (float)std::cos(angle), table[p * R + R / 2 + c] = (float)std::sin(angle);
+    }
+  g_err[0] = '\0';
+  return NVQ_OK;
+}
+
+namespace {
+
+// What the two rotating entries have in common.  Rows are left out by having no heads.
+nvq_status check_rope(const char* who, nvq::RopeRows& r, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, const int64_t in_st[3][2],
+                      const int64_t out_st[2][2], const float* q_weight, const float* k_weight, float eps, const float* table, int64_t P,
+                      int64_t R, int pairs, const int32_t* positions, int axes, const int32_t* sections) {
+  if (r.type < NVQ_TYPE_F32 || r.type > NVQ_TYPE_BF16) return fail(NVQ_ERR_RANGE, "%s: type=%d is not NVQ_TYPE_*", who, r.type);
+  if (r.out_type < NVQ_TYPE_F32 || r.out_type > NVQ_TYPE_BF16) return fail(NVQ_ERR_RANGE, "%s: out_type=%d is not NVQ_TYPE_*", who, r.out_type);
+  if (pairs != NVQ_ROPE_HALVES && pairs != NVQ_ROPE_NEIGHBOURS) return fail(NVQ_ERR_RANGE, "%s: pairs=%d is not NVQ_ROPE_*", who, pairs);
+  if (!(eps >= 0.0f) || eps > 3e38f) return fail(NVQ_ERR_RANGE, "%s: eps must be a number and not negative", who);
+  if (R < 4 || R > D || R % 4 != 0) return fail(NVQ_ERR_SHAPE, "%s: R=%lld must be a multiple of 4 in 4 .. D", who, (long long)R);
+  if (P < 1 || P >= kMaxDim) return fail(NVQ_ERR_SHAPE, "%s: P=%lld out of range", who, (long long)P);
+  if (axes < 1 || axes > 4) return fail(NVQ_ERR_RANGE, "%s: axes=%d outside 1 .. 4", who, axes);
+  if (axes == 1 && sections) return fail(NVQ_ERR_RANGE, "%s: one axis has no sections", who);
+  if (axes > 1 && !sections) return fail(NVQ_ERR_NULL, "%s: several axes need sections", who);
+  int64_t end = 0;
+  for (int i = 0; i < 3; ++i) r.ends[i] = (int)(R / 2);
+  for (int i = 0; axes > 1 && i < axes; ++i) {
+    if (sections[i] < 0 || sections[i] > R / 2) return fail(NVQ_ERR_RANGE, "%s: sections[%d]=%d out of range", who, i, (int)sections[i]);
+    end += sections[i];
+    if (i < 3) r.ends[i] = (int)end;
+  }
+  if (axes > 1 && end != R / 2) return fail(NVQ_ERR_RANGE, "%s: the sections must have R/2=%lld pairs in all", who, (long long)(R / 2));
+  if (T > 0) {
+    if (!table || !positions) return fail(NVQ_ERR_NULL, "%s: NULL pointer", who);
+    if (!aligned(table, 16) || !aligned(positions, 4) || !aligned(q_weight, 16) || !aligned(k_weight, 16))
+      return fail(NVQ_ERR_ALIGN, "%s: table and weights must be 16-byte aligned, positions 4-byte", who);
+    static const char* const names[] = {"q", "k", "v"};
+    const int64_t H[3] = {Hq, Hkv, Hkv};
+    for (int i = 0; i < 3; ++i)
+      if (r.heads[i]) NVQ_TRY(check_rows(who, names[i], r.in[i], r.type, T, H[i], in_st[i][0], in_st[i][1]));
+    for (int i = 0; i < 2; ++i)
+      if (r.out[i]) {
+        NVQ_TRY(check_rows(who, i ? "k_out" : "q_out", r.out[i], r.out_type, T, H[i], out_st[i][0], out_st[i][1]));
+        NVQ_TRY(check_apart(who, i ? "k_out" : "q_out", T, H[i], D, out_st[i][0], out_st[i][1]));
+      }
+  }
+  for (int i = 0; i < 3; ++i) r.in_t[i] = in_st[i][0], r.in_h[i] = in_st[i][1];
+  for (int i = 0; i < 2; ++i) r.out_t[i] = out_st[i][0], r.out_h[i] = out_st[i][1];
+  r.weight[0] = q_weight, r.weight[1] = k_weight;
+  r.eps = eps, r.table = table, r.n_pos = (int)P, r.rot = (int)R, r.neighbours = pairs == NVQ_ROPE_NEIGHBOURS;
+  r.positions = positions, r.axes = axes, r.axis_stride = T;
+  return NVQ_OK;
+}
+
+}  // namespace
+
+nvq_status nvq_qk_norm_rope(int type, int out_type, const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                            int64_t k_stride_t, int64_t k_stride_h, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                            const float* q_weight, const float* k_weight, float eps, const float* table, int64_t P, int64_t R,
+                            int pairs, const int32_t* positions, int axes, const int32_t* sections, void* q_out,
+                            int64_t qo_stride_t, int64_t qo_stride_h, void* k_out, int64_t ko_stride_t, int64_t ko_stride_h,
+                            void* stream) {
+  const char* who = "nvq_qk_norm_rope";
+  NVQ_TRY(check_head(who, Hkv, D));
+  if (Hq < 1 || Hq > 65536) return fail(NVQ_ERR_SHAPE, "%s: Hq=%lld outside [1, 65536]", who, (long long)Hq);
+  if (T < 0 || T >= kMaxDim / (Hq + Hkv)) return fail(NVQ_ERR_SHAPE, "%s: T=%lld out of range", who, (long long)T);
+  if (T > 0 && (!q != !q_out || !k != !k_out || (!q && !k)))
+    return fail(NVQ_ERR_NULL, "%s: q with q_out, k with k_out, or both", who);
+  nvq::RopeRows r = {};
+  r.type = type, r.out_type = out_type;
+  r.in[0] = q, r.in[1] = k, r.out[0] = q_out, r.out[1] = k_out;
+  r.heads[0] = q ? (uint32_t)Hq : 0, r.heads[1] = k ? (uint32_t)Hkv : 0;
+  const int64_t in_st[3][2] = {{q_stride_t, q_stride_h}, {k_stride_t, k_stride_h}, {0, 0}};
+  const int64_t out_st[2][2] = {{qo_stride_t, qo_stride_h}, {ko_stride_t, ko_stride_h}};
+  NVQ_TRY(check_rope(who, r, T, Hq, Hkv, D, in_st, out_st, q_weight, k_weight, eps, table, P, R, pairs, positions, axes, sections));
+  if (T == 0) return NVQ_OK;
+  NVQ_TRY(check_device());
+  return launched(nvq::launch_rope(r, T, D, -1, nullptr, nullptr, (hipStream_t)stream), who);
+}
+
+nvq_status nvq_rope_kv_write(int fmt, int type, int out_type, const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                             const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                             int64_t v_stride_h, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, const float* q_weight,
+                             const float* k_weight, float eps, const float* table, int64_t P, int64_t R, int pairs,
+                             const int32_t* positions, int axes, const int32_t* sections, const int64_t* slots, void* q_out,
+                             int64_t qo_stride_t, int64_t qo_stride_h, void* k_cache, void* v_cache, uint16_t* k_d,
+                             uint16_t* v_d, int64_t n_pages, int64_t page, void* stream) {
+  const char* who = "nvq_rope_kv_write";
+  nvq::KvCache c;
+  NVQ_TRY(check_cache(who, fmt, k_cache, v_cache, k_d, v_d, Hkv, D, n_pages, page, c));
+  if (Hq < 1 || Hq > 65536) return fail(NVQ_ERR_SHAPE, "%s: Hq=%lld outside [1, 65536]", who, (long long)Hq);
+  if (T < 0 || T >= kMaxDim / (Hq + 2 * Hkv)) return fail(NVQ_ERR_SHAPE, "%s: T=%lld out of range", who, (long long)T);
+  if (T > 0 && (!k || !v || !slots || !q != !q_out)) return fail(NVQ_ERR_NULL, "%s: NULL pointer (k, v and slots; q with q_out)", who);
+  nvq::RopeRows r = {};
+  r.type = type, r.out_type = out_type;
+  r.in[0] = q, r.in[1] = k, r.in[2] = v, r.out[0] = q_out;
+  r.heads[0] = q ? (uint32_t)Hq : 0, r.heads[1] = r.heads[2] = (uint32_t)Hkv;
+  const int64_t in_st[3][2] = {{q_stride_t, q_stride_h}, {k_stride_t, k_stride_h}, {v_stride_t, v_stride_h}};
+  const int64_t out_st[2][2] = {{qo_stride_t, qo_stride_h}, {0, 0}};
+  NVQ_TRY(check_rope(who, r, T, Hq, Hkv, D, in_st, out_st, q_weight, k_weight, eps, table, P, R, pairs, positions, axes, sections));
+  if (T > 0 && !aligned(slots, 8)) return fail(NVQ_ERR_ALIGN, "%s: slots must be 8-byte aligned", who);
+  if (T == 0) return NVQ_OK;
+  NVQ_TRY(check_device());
+  return launched(nvq::launch_rope(r, T, D, fmt, &c, slots, (hipStream_t)stream), who);
 }
 
 // One new token per sequence: the capacity in keys of all sequences stays below 2^30, so that

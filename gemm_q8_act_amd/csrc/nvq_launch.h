@@ -119,6 +119,26 @@ struct KvCache {
 // head stride, v's, in elements.
 hipError_t launch_kv_copy(bool write, int fmt, int type, const void* k, const void* v, const int64_t strides[4],
                           const int64_t* slots, int64_t T, int64_t heads, int64_t D, const KvCache& c, hipStream_t stream);
+// Norms and position rotation of query and key heads (rope.hip).  Rows of queries, keys and (into the cache)
+// values: in[], strides and heads of each, 0 heads where there are none.  Queries go to out[0], keys
+// to out[1], or with a cache format (fmt >= 0) keys and values to the cache rows at slots.
+struct RopeRows {
+  const void* in[3];
+  int64_t in_t[3], in_h[3];  // token and head strides, elements
+  void* out[2];
+  int64_t out_t[2], out_h[2];
+  const float* weight[2];  // null: no norm
+  const float* table;      // [n_pos][rot]: rot / 2 cosines, then sines
+  const int32_t* positions;  // [axes], axis_stride apart, [T]
+  int64_t axis_stride;
+  uint32_t heads[3];
+  int ends[3];  // pair number behind each axis' section but the last one's
+  float eps;
+  int n_pos, rot, neighbours, axes;
+  int type, out_type;
+};
+hipError_t launch_rope(const RopeRows& rows, int64_t T, int64_t D, int fmt, const KvCache* c, const int64_t* slots, hipStream_t stream);
+
 // Attention of one token per sequence over the cache (attn_decode.hip).
 hipError_t launch_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b, int64_t q_stride_h, int64_t B,
                               int64_t Hq, int64_t Hkv, int64_t D, const KvCache& c, const int32_t* table,

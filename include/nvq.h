@@ -493,6 +493,47 @@ nvq_status nvq_kv_read(int fmt, int type, void* k, int64_t k_stride_t, int64_t k
                        int64_t D, const void* k_cache, const void* v_cache, const uint16_t* k_d,
                        const uint16_t* v_d, int64_t n_pages, int64_t page, void* stream);
 
+/* The table of the position rotation (host memory, overwritten): row p of float32 [P][R] holds the
+ * cosines of p * inv_freq[c] for c = 0 .. R/2 - 1, then their sines, computed in double.  R a multiple
+ * of 4 up to 256, 1 <= P < 2^31. */
+nvq_status nvq_rope_table(const double* inv_freq, int64_t P, int64_t R, float* table);
+
+/* Norms of query and key heads and the position rotation, in one pass over the rows:
+ *     y = x * rsqrt(mean(x^2) + eps) * w     over the head's D channels, where a weight is given;
+ *     (a, b) -> (a cos - b sin, b cos + a sin)     for the R/2 pairs of the first R channels:
+ * pair c is channels c and c + R/2 (NVQ_ROPE_HALVES) or 2 c and 2 c + 1 (NVQ_ROPE_NEIGHBOURS); its cosine and
+ * sine are those of pair c in the table's row (float32 [P][R] on the device: nvq_rope_table's, or any
+ * with the same layout) at the token's position.  Channels from R on are normed only.
+ * positions: int32 [axes][T] on the device.  With 1 < axes <= 4, sections (host, int32 [axes], none
+ * negative, R/2 in all) says how many of the pairs, in order, take their position from each axis;
+ * with one axis it is NULL.  A position outside 0 .. P - 1 gives NaN in the pairs that it turns.
+ * q [T][Hq][D], k [T][Hkv][D] of `type`, q_out and k_out of `out_type` (each F32, F16 or BF16; strides
+ * between tokens and between heads, as for the cache).  Queries or keys may be left out: NULL with its
+ * output NULL.  An output may be its own input (same address, strides and type); otherwise it
+ * overlaps none of the inputs.  q_weight, k_weight: float32 [D] on the device, NULL: no norm of
+ * those heads; eps not negative.  R a multiple of 4, 4 <= R <= D; T * (Hq + Hkv) below 2^31.  Arithmetic
+ * and sums in float32, one rounding to out_type. */
+enum { NVQ_ROPE_HALVES = 0, NVQ_ROPE_NEIGHBOURS = 1 };
+nvq_status nvq_qk_norm_rope(int type, int out_type, const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                            int64_t k_stride_t, int64_t k_stride_h, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                            const float* q_weight, const float* k_weight, float eps, const float* table, int64_t P, int64_t R,
+                            int pairs, const int32_t* positions, int axes, const int32_t* sections, void* q_out,
+                            int64_t qo_stride_t, int64_t qo_stride_h, void* k_out, int64_t ko_stride_t, int64_t ko_stride_h,
+                            void* stream);
+
+/* The same on the way into the cache, in one launch: keys, normed and turned, and values, as they are,
+ * go to the cache rows at slots (as nvq_kv_write takes them; Q8_0 of the float32 result, or one rounding
+ * to 16 bits), queries, normed and turned, to q_out.  Without queries (q and q_out NULL) it is a write with
+ * rotation alone.  A key block with a NaN (a position outside the table) reads back as NaN.  Arguments as above
+ * and as nvq_kv_write's; T * (Hq + 2 Hkv) below 2^31. */
+nvq_status nvq_rope_kv_write(int fmt, int type, int out_type, const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                             const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                             int64_t v_stride_h, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, const float* q_weight,
+                             const float* k_weight, float eps, const float* table, int64_t P, int64_t R, int pairs,
+                             const int32_t* positions, int axes, const int32_t* sections, const int64_t* slots, void* q_out,
+                             int64_t qo_stride_t, int64_t qo_stride_h, void* k_cache, void* v_cache, uint16_t* k_d,
+                             uint16_t* v_d, int64_t n_pages, int64_t page, void* stream);
+
 /* Attention of one new token per sequence over the cache:
  *     out[b][h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q[b][h] . k_j),  j < lengths[b],
  * with k_j, v_j the cache rows of key head h / (Hq/Hkv) at place j of sequence b: page
