@@ -51,7 +51,8 @@ EXPORTS = (
     "nvq_q5_k_weight_bytes", "nvq_q6_k_weight_bytes", "nvq_pack_q5_k", "nvq_pack_q6_k",
     "nvq_gemv_q5_k", "nvq_gemm_q5_k", "nvq_gemv_q6_k", "nvq_gemm_q6_k",
     "nvq_kv_write", "nvq_kv_read", "nvq_attn_decode_workspace_bytes", "nvq_attn_decode", "nvq_attn_prompt",
-    "nvq_rope_table", "nvq_qk_norm_rope", "nvq_rope_kv_write",
+    "nvq_rope_table", "nvq_qk_norm_rope", "nvq_rope_kv_write", "nvq_attn_decode_window",
+    "nvq_attn_chunk_workspace_bytes", "nvq_attn_chunk",
     "nvq_status_str", "nvq_last_error",
     "nvq_probe_read", "nvq_probe_gemv_loads", "nvq_probe_mfma",
 )
@@ -122,6 +123,11 @@ def lib() -> ctypes.CDLL:
             "nvq_attn_decode_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I64]),
             "nvq_attn_decode": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, P, I64, I64, I64, I64, I64, I64, P, P, P, P,
                                                I64, I64, P, I64, P, F, P, P, SZ, P]),
+            "nvq_attn_decode_window": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, P, I64, I64, I64, I64, I64, I64, P, P, P, P,
+                                                      I64, I64, P, I64, P, F, I64, I64, P, P, SZ, P]),
+            "nvq_attn_chunk_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I64, I64, I64, I64]),
+            "nvq_attn_chunk": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, P, P, I64, I64, I64, I64, I64, P, P, P, P, I64, I64, P, I64, P, P, F, I64, I64,
+                                              P, P, SZ, P]),
             "nvq_attn_prompt": (ctypes.c_int, [ctypes.c_int, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, F,
                                                ctypes.c_int, P]),
             "nvq_rope_table": (ctypes.c_int, [P, I64, I64, P]),
@@ -916,11 +922,7 @@ def nvq_attn_decode_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, max_pages
     return int(lib().nvq_attn_decode_workspace_bytes(B, Hq, Hkv, D, max_pages, page))
 
 
-def nvq_attn_decode(q, k_cache, v_cache, table, lengths, out, k_d=None, v_d=None, scale=None, workspace=None,
-                    stream=None) -> None:
-    """One new token per sequence: q [B, Hq, D] (strides free), the paged cache, table int32 [B, max_pages] and
-    lengths int32 [B] -> out [B, Hq, D] of q's type.  scale: 1 / sqrt(D) unless given."""
-    L = _lib if _torch is not None else _attn_lib()
+def _attn_decode(fn, name, q, k_cache, v_cache, table, lengths, out, k_d, v_d, scale, window, sinks, more, workspace, stream):
     here = -1
     try:
         fmt, shape, rows, dtype = _cache_types[k_cache.dtype], k_cache.shape, q.shape, q.dtype
@@ -949,14 +951,32 @@ def nvq_attn_decode(q, k_cache, v_cache, table, lengths, out, k_d=None, v_d=None
         _wrong_device(q, k_cache, v_cache, table, lengths, out, k_d, v_d, workspace)
         raise ValueError("q, out, the cache, table, lengths and workspace do not fit together (all but q contiguous)")
     if workspace is None:
-        workspace = _workspace(nvq_attn_decode_workspace_bytes(B, Hq, heads, D, max_pages, page), stream, q)
+        pages = max_pages if not window else min(max_pages, (window + sinks + 30) // max(page, 1) + 1)  # a longer table's other pages are not read
+        workspace = _workspace(nvq_attn_decode_workspace_bytes(B, Hq, heads, D, pages, page), stream, q)
     wp, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = L.nvq_attn_decode(fmt, code, q.data_ptr(), qs[0], qs[1], B, Hq, heads, D, k_cache.data_ptr(), v_cache.data_ptr(),
-                           None if fmt else k_d.data_ptr(), None if fmt else v_d.data_ptr(), n_pages, page, table.data_ptr(), max_pages,
-                           lengths.data_ptr(), max(D, 1) ** -0.5 if scale is None else scale, out.data_ptr(), wp, ws_bytes,
-                           _torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream))
+    st = fn(fmt, code, q.data_ptr(), qs[0], qs[1], B, Hq, heads, D, k_cache.data_ptr(), v_cache.data_ptr(),
+            None if fmt else k_d.data_ptr(), None if fmt else v_d.data_ptr(), n_pages, page, table.data_ptr(), max_pages,
+            lengths.data_ptr(), max(D, 1) ** -0.5 if scale is None else scale, *more, out.data_ptr(), wp, ws_bytes,
+            _torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream))
     if st:
-        _check(st, "nvq_attn_decode")
+        _check(st, name)
+
+
+def nvq_attn_decode(q, k_cache, v_cache, table, lengths, out, k_d=None, v_d=None, scale=None, workspace=None,
+                    stream=None) -> None:
+    """One new token per sequence: q [B, Hq, D] (strides free), the paged cache, table int32 [B, max_pages] and
+    lengths int32 [B] -> out [B, Hq, D] of q's type.  scale: 1 / sqrt(D) unless given."""
+    L = _lib if _torch is not None else _attn_lib()
+    _attn_decode(L.nvq_attn_decode, "nvq_attn_decode", q, k_cache, v_cache, table, lengths, out, k_d, v_d, scale, 0, 0, (), workspace, stream)
+
+
+def nvq_attn_decode_window(q, k_cache, v_cache, table, lengths, out, k_d=None, v_d=None, window=0, sinks=0, scale=None, workspace=None,
+                           stream=None) -> None:
+    """nvq_attn_decode over the last `window` keys of each sequence (0: all) and its first `sinks`; the other pages may be
+    gone."""
+    L = _lib if _torch is not None else _attn_lib()
+    _attn_decode(L.nvq_attn_decode_window, "nvq_attn_decode_window", q, k_cache, v_cache, table, lengths, out, k_d, v_d, scale, window, sinks,
+                 (window, sinks), workspace, stream)
 
 
 def nvq_attn_prompt(q, k, v, cu_q, cu_k, out, scale=None, causal=True, stream=None) -> None:
@@ -999,6 +1019,60 @@ def nvq_attn_prompt(q, k, v, cu_q, cu_k, out, scale=None, causal=True, stream=No
 
 
 _Strides = ctypes.c_int64 * 8
+_Strides4 = ctypes.c_int64 * 4
+
+
+@functools.lru_cache(maxsize=256)
+def nvq_attn_chunk_workspace_bytes(B: int, Tq: int, Hq: int, Hkv: int, D: int, max_pages: int, page: int, window: int = 0, sinks: int = 0) -> int:
+    return int(lib().nvq_attn_chunk_workspace_bytes(B, Tq, Hq, Hkv, D, max_pages, page, window, sinks))
+
+
+def nvq_attn_chunk(q, k_cache, v_cache, table, cu_q, lengths, out, k_d=None, v_d=None, window=0, sinks=0, scale=None, workspace=None,
+                   stream=None) -> None:
+    """New tokens over the paged cache that holds them: q [Tq, Hq, D] (float16 or bfloat16, a 16-bit cache's type; strides free)
+    packed by cu_q int32 [B+1], table int32 [B, max_pages], lengths int32 [B] (keys, the new tokens' among them) -> out
+    [Tq, Hq, D] (strides free).  Query i of m sees keys j <= p = i + n - m of its n; with a window those of j > p - window or
+    j < sinks.  scale: 1 / sqrt(D) unless given."""
+    L = _lib if _torch is not None else _attn_lib()
+    here = -1
+    try:
+        fmt, shape, rows, dtype = _cache_types[k_cache.dtype], k_cache.shape, q.shape, q.dtype
+        n_pages, heads, page, D = shape
+        Tq, Hq, _ = rows
+        B, max_pages = table.shape
+        qs, ps, code, i32 = q.stride(), out.stride(), _row_types[dtype], _torch.int32
+        fine = (_cache_fine(fmt, shape, k_cache, v_cache, k_d, v_d) and rows == (Tq, Hq, D) and out.shape == rows and out.dtype is dtype
+                and qs[2] == 1 and ps[2] == 1 and table.dtype is i32 and table.is_contiguous() and cu_q.dtype is i32 and cu_q.shape == (B + 1,)
+                and cu_q.is_contiguous() and lengths.dtype is i32 and lengths.shape == (B,) and lengths.is_contiguous())
+        if fine:
+            here = _torch.cuda.current_device()
+            fine = (q.get_device() == here and out.get_device() == here and k_cache.get_device() == here and v_cache.get_device() == here
+                    and table.get_device() == here and cu_q.get_device() == here and lengths.get_device() == here
+                    and (fmt or k_d.get_device() == here and v_d.get_device() == here)
+                    and (workspace is None or workspace.get_device() == here and workspace.is_contiguous()))
+    except (AttributeError, KeyError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _wrong_cache(k_cache, v_cache, k_d, v_d)
+        shape = (*(q.shape[:2] if q is not None and q.dim() == 3 else (-1, -1)), k_cache.shape[3])
+        _wrong_rows(q, q.dtype if q is not None else None, shape, "q")
+        _wrong_rows(out, q.dtype, shape, "out")
+        if table is None or table.dim() != 2:
+            raise ValueError("table: int32 [B, max_pages] is required")
+        _wrong_dense(table, _torch.int32, table.shape, "table")
+        _wrong_dense(cu_q, _torch.int32, (table.shape[0] + 1,), "cu_q")
+        _wrong_dense(lengths, _torch.int32, table.shape[:1], "lengths")
+        _wrong_device(q, k_cache, v_cache, table, cu_q, lengths, out, k_d, v_d, workspace)
+        raise ValueError("q, out, the cache, table, cu_q, lengths and workspace do not fit together")
+    if workspace is None:
+        workspace = _workspace(nvq_attn_chunk_workspace_bytes(B, Tq, Hq, heads, D, max_pages, page, window, sinks), stream, q)
+    wp, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = L.nvq_attn_chunk(fmt, code, q.data_ptr(), _Strides4(qs[0], qs[1], ps[0], ps[1]), B, Tq, Hq, heads, D, k_cache.data_ptr(), v_cache.data_ptr(),
+                          None if fmt else k_d.data_ptr(), None if fmt else v_d.data_ptr(), n_pages, page, table.data_ptr(), max_pages,
+                          cu_q.data_ptr(), lengths.data_ptr(), max(D, 1) ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), wp, ws_bytes,
+                          _torch._C._cuda_getCurrentRawStream(here) if stream is None else int(stream))
+    if st:
+        _check(st, "nvq_attn_chunk")
 
 
 # ---------------------------------------------------------------------------

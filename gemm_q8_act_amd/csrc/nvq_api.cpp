@@ -839,14 +839,15 @@ size_t nvq_attn_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64
   return nvq::attn_decode_workspace(B, Hq, Hkv, D, max_pages * page);
 }
 
-nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b, int64_t q_stride_h, int64_t B, int64_t Hq,
-                           int64_t Hkv, int64_t D, const void* k_cache, const void* v_cache, const uint16_t* k_d,
-                           const uint16_t* v_d, int64_t n_pages, int64_t page, const int32_t* table, int64_t max_pages,
-                           const int32_t* lengths, float scale, void* out, void* workspace, size_t ws_bytes, void* stream) {
-  const char* who = "nvq_attn_decode";
+static nvq_status attn_decode(const char* who, int fmt, int type, const void* q, int64_t q_stride_b, int64_t q_stride_h, int64_t B,
+                              int64_t Hq, int64_t Hkv, int64_t D, const void* k_cache, const void* v_cache, const uint16_t* k_d,
+                              const uint16_t* v_d, int64_t n_pages, int64_t page, const int32_t* table, int64_t max_pages,
+                              const int32_t* lengths, float scale, int64_t window, int64_t sinks, void* out, void* workspace,
+                              size_t ws_bytes, void* stream) {
   if (type < NVQ_TYPE_F32 || type > NVQ_TYPE_BF16) return fail(NVQ_ERR_RANGE, "%s: type=%d is not NVQ_TYPE_*", who, type);
   nvq::KvCache c;
   NVQ_TRY(check_cache(who, fmt, k_cache, v_cache, k_d, v_d, Hkv, D, n_pages, page, c));
+  if (window < 0 || sinks < 0) return fail(NVQ_ERR_RANGE, "%s: window=%lld and sinks=%lld must not be negative", who, (long long)window, (long long)sinks);
   if (B == 0) return NVQ_OK;
   if (!decode_shape_ok(B, Hq, Hkv, D, max_pages, page))
     return fail(NVQ_ERR_SHAPE, "%s: B=%lld, Hq=%lld, Hkv=%lld, max_pages=%lld, page=%lld out of range (Hq a multiple of Hkv, B * max_pages * page < 2^30, B * Hkv * ceil(Hq / Hkv / 16) < 2^23)",
@@ -855,12 +856,35 @@ nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b,
   NVQ_TRY(check_rows(who, "q", q, type, B, Hq, q_stride_b, q_stride_h));
   if (!aligned(out, 16) || !aligned(table, 4) || !aligned(lengths, 4))
     return fail(NVQ_ERR_ALIGN, "%s: out must be 16-byte aligned, table and lengths 4-byte", who);
-  const size_t need = nvq::attn_decode_workspace(B, Hq, Hkv, D, max_pages * page);
+  // (no sequence has more keys than the tables' pages hold; a window of them all, or first keys that are all, is none)
+  const int64_t keys = max_pages * page;
+  if (window >= keys || sinks >= keys) window = 0;
+  const size_t need = nvq::attn_decode_workspace(B, Hq, Hkv, D, window ? nvq::attn_window_capacity(keys, window, sinks) : keys);
   if (need > 0 && (!workspace || ws_bytes < need)) return fail(NVQ_ERR_WORKSPACE, "%s: workspace of %zu bytes required, got %zu", who, need, workspace ? ws_bytes : (size_t)0);
   if (need > 0 && !aligned(workspace, 16)) return fail(NVQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", who);
   NVQ_TRY(check_device());
+  if (window)
+    return launched(nvq::launch_attn_decode_window(fmt, type, q, q_stride_b, q_stride_h, B, Hq, Hkv, D, c, table, max_pages, lengths, scale,
+                                                   (int)window, (int)sinks, out, workspace, (hipStream_t)stream), who);
   return launched(nvq::launch_attn_decode(fmt, type, q, q_stride_b, q_stride_h, B, Hq, Hkv, D, c, table, max_pages, lengths, scale, out,
                                           workspace, (hipStream_t)stream), who);
+}
+
+nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b, int64_t q_stride_h, int64_t B, int64_t Hq,
+                           int64_t Hkv, int64_t D, const void* k_cache, const void* v_cache, const uint16_t* k_d,
+                           const uint16_t* v_d, int64_t n_pages, int64_t page, const int32_t* table, int64_t max_pages,
+                           const int32_t* lengths, float scale, void* out, void* workspace, size_t ws_bytes, void* stream) {
+  return attn_decode("nvq_attn_decode", fmt, type, q, q_stride_b, q_stride_h, B, Hq, Hkv, D, k_cache, v_cache, k_d, v_d, n_pages, page, table,
+                     max_pages, lengths, scale, 0, 0, out, workspace, ws_bytes, stream);
+}
+
+nvq_status nvq_attn_decode_window(int fmt, int type, const void* q, int64_t q_stride_b, int64_t q_stride_h, int64_t B, int64_t Hq,
+                                  int64_t Hkv, int64_t D, const void* k_cache, const void* v_cache, const uint16_t* k_d,
+                                  const uint16_t* v_d, int64_t n_pages, int64_t page, const int32_t* table, int64_t max_pages,
+                                  const int32_t* lengths, float scale, int64_t window, int64_t sinks, void* out, void* workspace,
+                                  size_t ws_bytes, void* stream) {
+  return attn_decode("nvq_attn_decode_window", fmt, type, q, q_stride_b, q_stride_h, B, Hq, Hkv, D, k_cache, v_cache, k_d, v_d, n_pages, page,
+                     table, max_pages, lengths, scale, window, sinks, out, workspace, ws_bytes, stream);
 }
 
 nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v, void* out, const int64_t* strides,
@@ -889,6 +913,54 @@ nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v
   NVQ_TRY(check_device());
   return launched(nvq::launch_attn_prompt(type, q, k, v, out, strides, cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, scale, causal ? 1 : 0,
                                           (hipStream_t)stream), who);
+}
+
+static bool chunk_shape_ok(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages, int64_t page) {
+  constexpr int64_t most = int64_t(1) << 30;
+  return B >= 1 && B < most && Tq >= 1 && Tq < most && Hkv >= 1 && Hkv <= 65536 && Hq >= Hkv && Hq <= 65536 && Hq % Hkv == 0 && D >= 32 && D <= 256 &&
+         D % 32 == 0 && page_ok(page) && max_pages >= 1 && max_pages < most / page && nvq::attn_chunk_fits(B, Tq, Hq, Hkv, max_pages * page);
+}
+
+// A window of all keys that the tables' pages can hold, or first keys that are all of them, is none.
+static int64_t chunk_window(int64_t keys, int64_t window, int64_t sinks) { return window >= keys || sinks >= keys ? 0 : window; }
+
+size_t nvq_attn_chunk_workspace_bytes(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages, int64_t page,
+                                      int64_t window, int64_t sinks) {
+  if (!chunk_shape_ok(B, Tq, Hq, Hkv, D, max_pages, page) || window < 0 || sinks < 0) return 0;
+  return nvq::attn_chunk_workspace(B, Tq, Hq, Hkv, D, max_pages * page, chunk_window(max_pages * page, window, sinks), sinks);
+}
+
+nvq_status nvq_attn_chunk(int fmt, int type, const void* q, const int64_t* strides, int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv,
+                          int64_t D, const void* k_cache, const void* v_cache, const uint16_t* k_d, const uint16_t* v_d,
+                          int64_t n_pages, int64_t page, const int32_t* table, int64_t max_pages, const int32_t* cu_q,
+                          const int32_t* lengths, float scale, int64_t window, int64_t sinks, void* out, void* workspace,
+                          size_t ws_bytes, void* stream) {
+  const char* who = "nvq_attn_chunk";
+  if (type != NVQ_TYPE_F16 && type != NVQ_TYPE_BF16) return fail(NVQ_ERR_RANGE, "%s: type=%d must be NVQ_TYPE_F16 or NVQ_TYPE_BF16", who, type);
+  nvq::KvCache c;
+  NVQ_TRY(check_cache(who, fmt, k_cache, v_cache, k_d, v_d, Hkv, D, n_pages, page, c));
+  if (fmt != NVQ_KV_Q8_0 && (fmt == NVQ_KV_F16) != (type == NVQ_TYPE_F16))
+    return fail(NVQ_ERR_RANGE, "%s: queries over a 16-bit cache must be of its type", who);
+  if (window < 0 || sinks < 0) return fail(NVQ_ERR_RANGE, "%s: window=%lld and sinks=%lld must not be negative", who, (long long)window, (long long)sinks);
+  if (B < 0 || Tq < 0) return fail(NVQ_ERR_SHAPE, "%s: B=%lld, Tq=%lld out of range", who, (long long)B, (long long)Tq);
+  if (B == 0 || Tq == 0) return NVQ_OK;
+  if (!chunk_shape_ok(B, Tq, Hq, Hkv, D, max_pages, page))
+    return fail(NVQ_ERR_SHAPE, "%s: B=%lld, Tq=%lld, Hq=%lld, Hkv=%lld, max_pages=%lld, page=%lld out of range (Hq a multiple of Hkv, max_pages * page < 2^30, "
+                "(Tq * Hq / Hkv / 128 + B) * ceil(max_pages * page / 64) < 2^31, (Tq * Hq / Hkv / 128 + B) * Hkv < 2^24 - 512)",
+                who, (long long)B, (long long)Tq, (long long)Hq, (long long)Hkv, (long long)max_pages, (long long)page);
+  if (!q || !strides || !table || !cu_q || !lengths || !out) return fail(NVQ_ERR_NULL, "%s: NULL pointer", who);
+  NVQ_TRY(check_rows(who, "q", q, type, Tq, Hq, strides[0], strides[1]));
+  NVQ_TRY(check_rows(who, "out", out, type, Tq, Hq, strides[2], strides[3]));
+  NVQ_TRY(check_apart(who, "out", Tq, Hq, D, strides[2], strides[3]));
+  if (!aligned(table, 4) || !aligned(cu_q, 4) || !aligned(lengths, 4)) return fail(NVQ_ERR_ALIGN, "%s: table, cu_q and lengths must be 4-byte aligned", who);
+  const int64_t keys = max_pages * page;
+  window = chunk_window(keys, window, sinks);
+  const size_t need = nvq::attn_chunk_workspace(B, Tq, Hq, Hkv, D, keys, window, sinks);
+  if (need > 0 && (!workspace || ws_bytes < need)) return fail(NVQ_ERR_WORKSPACE, "%s: workspace of %zu bytes required, got %zu", who, need, workspace ? ws_bytes : (size_t)0);
+  if (need > 0 && !aligned(workspace, 16)) return fail(NVQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", who);
+  NVQ_TRY(check_device());
+  return launched(nvq::launch_attn_chunk(fmt, type, q, out, strides, B, Tq, Hq, Hkv, D, c, table, max_pages, cu_q, lengths, (int)window,
+                                         window ? (int)sinks : 0, scale, workspace, (hipStream_t)stream), who);
 }
 
 // ---- measurement probes (include/nvq_probe.h) ----

@@ -144,6 +144,13 @@ hipError_t launch_attn_decode(int fmt, int type, const void* q, int64_t q_stride
                               int64_t Hq, int64_t Hkv, int64_t D, const KvCache& c, const int32_t* table,
                               int64_t table_stride, const int32_t* lengths, float scale, void* out, void* workspace,
                               hipStream_t stream);
+// The same over the last `window` keys (at least 1) and the first `sinks`: its workspace, and whether it fits, are those
+// of a capacity of attn_window_capacity keys (attn_decode_window.hip).
+hipError_t launch_attn_decode_window(int fmt, int type, const void* q, int64_t q_stride_b, int64_t q_stride_h, int64_t B,
+                                     int64_t Hq, int64_t Hkv, int64_t D, const KvCache& c, const int32_t* table,
+                                     int64_t table_stride, const int32_t* lengths, float scale, int window, int sinks, void* out,
+                                     void* workspace, hipStream_t stream);
+int64_t attn_window_capacity(int64_t capacity, int64_t window, int64_t sinks);
 size_t attn_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity);
 // Whether its launches (and prompt attention's) stay below 2^32 threads: a longer one would be cut short
 // without an error.
@@ -155,6 +162,15 @@ bool attn_prompt_fits(int64_t B, int64_t Tq, int64_t Hq);
 hipError_t launch_attn_prompt(int type, const void* q, const void* k, const void* v, void* out, const int64_t strides[8],
                               const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,
                               int64_t Hkv, int64_t D, float scale, int causal, hipStream_t stream);
+
+// Causal attention of several new tokens per sequence over the cache (attn_chunk.hip); strides: token and head
+// stride of q and out, in elements.  window 0: none.
+hipError_t launch_attn_chunk(int fmt, int type, const void* q, void* out, const int64_t strides[4], int64_t B, int64_t Tq, int64_t Hq,
+                             int64_t Hkv, int64_t D, const KvCache& c, const int32_t* table, int64_t table_stride, const int32_t* cu_q,
+                             const int32_t* lengths, int window, int sinks, float scale, void* workspace, hipStream_t stream);
+size_t attn_chunk_workspace(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity, int64_t window, int64_t sinks);
+// Whether its tile counts fit 31 bits and its launches stay below 2^32 threads.
+bool attn_chunk_fits(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t capacity);
 
 // Measurement probes (probe.hip): a streaming read of n16 16-byte units over `blocks`
 // blocks of 256 threads (sink: 4 words per block); the decode GEMV's weight loads

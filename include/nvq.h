@@ -558,6 +558,18 @@ nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b,
                            const int32_t* table, int64_t max_pages, const int32_t* lengths, float scale, void* out,
                            void* workspace, size_t ws_bytes, void* stream);
 
+/* The same with a sliding window and first keys that stay visible: of a sequence of n keys its one new token
+ * sees key j only if j >= n - window or j < sinks; window 0: all of them.  Pages that hold no such key are not
+ * looked up, so their table entries may be anything; the rest of a 16-key group (from a multiple of 16 on)
+ * that holds one never matters, whatever it holds.  Arguments and errors as above; window and sinks not negative.
+ * nvq_attn_decode_workspace_bytes of the same shape is enough, or of as few pages as hold
+ * window + sinks + 30 keys. */
+nvq_status nvq_attn_decode_window(int fmt, int type, const void* q, int64_t q_stride_b, int64_t q_stride_h, int64_t B,
+                                  int64_t Hq, int64_t Hkv, int64_t D, const void* k_cache, const void* v_cache,
+                                  const uint16_t* k_d, const uint16_t* v_d, int64_t n_pages, int64_t page,
+                                  const int32_t* table, int64_t max_pages, const int32_t* lengths, float scale,
+                                  int64_t window, int64_t sinks, void* out, void* workspace, size_t ws_bytes, void* stream);
+
 /* Attention of whole prompts, packed one behind the other: sequence b's queries are rows
  * cu_q[b] .. cu_q[b+1] - 1 of q [Tq][Hq][D], its keys and values rows cu_k[b] .. cu_k[b+1] - 1
  * of k, v [Tk][Hkv][D] (int32 [B+1] on the device, ascending from 0).  With m queries and n
@@ -575,6 +587,38 @@ nvq_status nvq_attn_decode(int fmt, int type, const void* q, int64_t q_stride_b,
 nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v, void* out,
                            const int64_t* strides, const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq,
                            int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, float scale, int causal, void* stream);
+
+/* Causal attention of the new tokens of each sequence over the cache, which holds them already and
+ * everything before them: sequence b's queries are rows cu_q[b] .. cu_q[b+1] - 1 of q [Tq][Hq][D] (int32 [B+1] on
+ * the device, ascending from 0), its keys and values the lengths[b] rows that its line of the table names (as
+ * nvq_attn_decode's).  With m queries and n keys, query i stands at place p = i + n - m and sees key j if
+ * j <= p and, with a window (0: none), j > p - window or j < sinks.  A query that sees no key (m > n) gives zeros.
+ * So a piece of a prompt, a few speculated tokens, single tokens and a batch of all these are one
+ * call.  `type` NVQ_TYPE_F16 or BF16; a 16-bit cache has the queries' type.  strides[4]: token and head
+ * stride of q and out (host).  Hq a multiple of Hkv; max_pages * page < 2^30;
+ * (Tq * Hq/Hkv / 128 + B) * ceil(max_pages * page / 64) < 2^31; (Tq * Hq/Hkv / 128 + B) * Hkv < 2^24 - 512.
+ * Rows of out in no sequence are left alone; offsets outside q are cut to it.  A length outside
+ * 0 .. max_pages * page gives NaN in all of the sequence's rows; a page number outside the cache, among the
+ * pages of keys that a query sees, NaN in that query's row and perhaps in others of its sequence (nothing is read
+ * there).  Pages whose keys no query sees (before the windows, behind the end) are not looked up.
+ * Scores, softmax statistics and accumulation are float32; the probabilities enter the second product rounded
+ * once to 16 bits (binary16 over Q8_0: 11 bits down to 2^-25 of the largest, as in nvq_attn_prompt).  Over
+ * Q8_0 the operands are code * scale rounded to binary16's 11 bits: of keys down to 2^-36 of the largest in
+ * their 64-key tile, of values down to 2^-36 of the largest that the query's tiles have had so far; bfloat16
+ * queries' channels are held to 2^-32 of the largest.  Keys and values that a query does not see never
+ * matter, whatever they hold.  An infinity or NaN in a value row shows, as one of them, in its channel (over
+ * Q8_0 in its 32-channel block) of the queries that see it, in a key row in all of theirs.  out overlaps none of
+ * the inputs.
+ * workspace: device, at least nvq_attn_chunk_workspace_bytes, contents irrelevant, overwritten; NULL when that
+ * is 0.  Calls that share it must not overlap in time.  The bytes of more tokens, sequences or pages, or of no
+ * window, are enough for fewer, or for a window. */
+size_t nvq_attn_chunk_workspace_bytes(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages,
+                                      int64_t page, int64_t window, int64_t sinks);
+nvq_status nvq_attn_chunk(int fmt, int type, const void* q, const int64_t* strides, int64_t B, int64_t Tq, int64_t Hq,
+                          int64_t Hkv, int64_t D, const void* k_cache, const void* v_cache, const uint16_t* k_d,
+                          const uint16_t* v_d, int64_t n_pages, int64_t page, const int32_t* table, int64_t max_pages,
+                          const int32_t* cu_q, const int32_t* lengths, float scale, int64_t window, int64_t sinks, void* out,
+                          void* workspace, size_t ws_bytes, void* stream);
 
 /* ---- debug: integer per-16 partial sums --------------------------------------- */
 
