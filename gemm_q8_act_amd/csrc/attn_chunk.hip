@@ -24,8 +24,12 @@ namespace {
 
 constexpr int kWaves = kTileWaves;
 constexpr int kRows = 32 * kWaves;  // of a workgroup
-constexpr int kMinPart = 2;         // tiles: the shortest part
-constexpr int kTargetGroups = 512;
+constexpr int kMinPart = 2;  // tiles: the shortest part
+// Parts for one round of workgroups over the chip, or for two where a workgroup's share of the call is more than
+// this many tiles (the last round's idle places then cost less).
+constexpr int kOneRound = 32, kRounds = 2;
+// Workgroups that the chip holds at once (by registers), for nb 32-blocks a row
+constexpr int places(int nb) { return 256 * (nb <= 2 ? 3 : nb <= 4 ? 2 : 1); }
 
 struct ChunkArgs {
   const uint16_t* q;
@@ -41,7 +45,7 @@ struct ChunkArgs {
   int B, Hq, Hkv, G, Tq;
   int window, sinks;
   int type;
-  int target;      // parts wanted of a key head
+  int places;      // workgroups at once of a key head
   int slot_waves;  // wavefronts' rows that a part's slot holds
 };
 
@@ -51,6 +55,10 @@ __device__ __forceinline__ int tiles_seen(const ChunkArgs& a, int n) {
   const int all = (n + kKeys - 1) / kKeys;
   return min(all, (min(a.sinks, n) + kKeys - 1) / kKeys + (a.window + kRows - 1 + kKeys - 1) / kKeys + 1);
 }
+
+// A value that all lanes share, in a scalar register (what a division leaves in a vector one would drag all that
+// follows along)
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 struct Seq {
   int q0, m, n;    // first query, number of them, and keys (0 if out of range, and bad is set)
@@ -72,15 +80,15 @@ __device__ __forceinline__ Seq load_seq(const ChunkArgs& a, int i) {
   return s;
 }
 
-// How the work is cut: the key tiles of a row tile go in parts of `part_tiles`, of a length for the whole
-// call that makes about `target` parts of a key head.
+// How the work is cut: the key tiles of a row tile go in equal parts of `part_tiles`, at most of a length for the
+// whole call that makes about as many parts as the chip has places for, or twice that.
 struct Work {
   Seq s;
   int b;            // sequence, -1: no such work
   int tile;         // row tile of it
   int part;         // part of the tile (main kernel)
   int parts;        // parts that its row tiles have at most
-  int part_tiles;
+  int part_tiles;   // key tiles of a part
   int slot;         // of the part, or of the row tile's first part; -1: the sequence is not split
 };
 
@@ -88,19 +96,23 @@ struct Work {
 // the most keys, come first.
 __device__ __forceinline__ Work find_work(const ChunkArgs& a, int want, bool join) {
   const int lane = (int)(threadIdx.x & 63);
-  int total = 0;  // (below 2^31: host check)
-  for (int i = lane; i - lane < a.B; i += 64) {
-    const Seq s = load_seq(a, i);
-    total += s.tiles * s.most;
+  int total = 0, all = 0;  // key tiles of all row tiles (below 2^31: host check), and row tiles
+  for (int i0 = 0; i0 < a.B; i0 += 64) {
+    const Seq s = load_seq(a, i0 + lane);
+    total += s.tiles * s.most, all += s.tiles;
   }
   total = __builtin_amdgcn_readlane(wave_running_sum(total), 63);
-  Work w;
-  w.part_tiles = max(kMinPart, (int)(((uint32_t)total + (uint32_t)a.target - 1) / (uint32_t)a.target));
+  Work w = {};
+  all = __builtin_amdgcn_readlane(wave_running_sum(all), 63);
+  // (a row tile's last part is a part of one: half of one is taken off for each)
+  const int rounds = total / kOneRound > a.places ? kRounds : 1;
+  const uint32_t whole = (uint32_t)max(rounds * a.places - all / 2, (a.places + 3) / 4);
+  const int most = uniform(max(kMinPart, (int)(((uint32_t)total + whole - 1) / whole)));
   w.b = -1;
   int base = 0, slots = 0;
   for (int i0 = 0; i0 < a.B; i0 += 64) {
     const Seq s = load_seq(a, i0 + lane);
-    const int parts = max(1, (s.most + w.part_tiles - 1) / w.part_tiles);
+    const int parts = max(1, (s.most + most - 1) / most);
     const int taken = parts > 1 ? s.tiles * parts : 0;
     const int mine = join ? (parts > 1 ? s.tiles : 0) : s.tiles * parts;
     const int incl = wave_running_sum(mine), incl_slots = wave_running_sum(taken);
@@ -111,8 +123,9 @@ __device__ __forceinline__ Work find_work(const ChunkArgs& a, int want, bool joi
       w.b = i0 + l;
       w.s = {of(s.q0), of(s.m), of(s.n), of(s.tiles), of(s.most), of((int)s.bad) != 0};
       w.parts = of(parts);
+      w.part_tiles = max(1, uniform((w.s.most + w.parts - 1) / w.parts));  // parts of equal length
       const int at = want - (base + of(incl) - of(mine));
-      const int turn = join ? at : at / w.parts;
+      const int turn = join ? at : uniform(at / w.parts);
       w.part = join ? 0 : at - turn * w.parts;
       w.tile = w.s.tiles - 1 - turn;
       w.slot = w.parts > 1 ? slots + of(incl_slots) - of(taken) + turn * w.parts + w.part : -1;
@@ -138,7 +151,7 @@ __device__ __forceinline__ Rows rows_of(const ChunkArgs& a, const Work& w) {
   const int rows = w.s.m * a.G, shift = w.s.n - w.s.m;
   r.r0 = w.tile * kRows;
   r.count = min(kRows, rows - r.r0);
-  r.first = r.r0 / a.G + shift, r.last = (r.r0 + r.count - 1) / a.G + shift;
+  r.first = uniform(r.r0 / a.G) + shift, r.last = uniform((r.r0 + r.count - 1) / a.G) + shift;
   r.end = min(max(r.last + 1, 0), w.s.n);
   r.start = max(r.first - a.window + 1, 0);
   r.sink = min(a.sinks, r.start);
@@ -152,8 +165,8 @@ template <int FMT, int NB>
 struct Cached {
   static constexpr bool Q8 = FMT == NVQ_KV_Q8_0;
   static constexpr int ROW = Q8 ? 32 * NB : 64 * NB;  // bytes of a cache row
-  static constexpr int WORDS = ROW / 16;              // dwords that a lane stages of it (4 lanes to a row)
-  static constexpr int SCALES = Q8 ? NB : 1;
+  static constexpr int WORDS = Q8 ? 2 * NB : 1;       // Q8_0: dwords that a lane takes of it (4 lanes to a row)
+  static constexpr int SCALES = Q8 ? (NB + 1) / 2 : 1;  // its scales, two a dword
 };
 
 // The channel of place p of a row's order in the cache
@@ -164,9 +177,15 @@ __device__ __forceinline__ int channel_of(int p) {
   return 32 * (pair % NB) + 2 * (pair / NB) + (p & 1);
 }
 
+// N dwords, as a vector: an array that is copied about would be kept in memory
+template <int N>
+struct Dwords {
+  typedef uint32_t type __attribute__((ext_vector_type(N)));
+};
 // N dwords of a buffer from a byte offset that is a multiple of 4 N up to 16
 template <int N>
-__device__ __forceinline__ void load_dwords(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t* v) {
+__device__ __forceinline__ typename Dwords<N>::type load_dwords(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  typename Dwords<N>::type v;
   if constexpr (N % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
@@ -174,14 +193,17 @@ __device__ __forceinline__ void load_dwords(__amdgpu_buffer_rsrc_t r, uint32_t a
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[4 * i + j] = t[j];
     }
-  } else {
-    static_assert(N % 2 == 0, "pairs of dwords");
+  } else if constexpr (N % 2 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
       const u32x2 t = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, at + 8 * i, 0, 0));
       v[2 * i] = t[0], v[2 * i + 1] = t[1];
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b32(r, at + 4 * i, 0, 0);
   }
+  return v;
 }
 
 // Which of a pair of 16-bit elements are not finite: their bits set
@@ -191,62 +213,266 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   return ((w & e) == e ? 0xFFFFu : 0u) | (((w >> 16) & e) == e ? 0xFFFF0000u : 0u);
 }
 
-// Largest of a wavefront's unsigned values
-__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a), __builtin_bit_cast(u16x2_t, b)));
+}
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) { return w & 0x7FFF7FFFu & ~not_finite<_Float16>(w); }
+
+// Largest of a lane's scales, both halves; and over a wavefront whose quads hold the same, in the upper
+// half of a and of b: the result's halves
+template <int N>
+__device__ __forceinline__ uint32_t largest_scale(typename Dwords<N>::type d) {
+  uint32_t x = 0;
 #pragma unroll
-  for (int step = 1; step < 64; step *= 2) v = max(v, (uint32_t)__shfl_xor((int)v, step));
-  return v;
+  for (int i = 0; i < N; ++i) x = max_halves(x, finite_halves(d[i]));
+  return max_halves(x, x << 16);
+}
+__device__ __forceinline__ uint32_t wave_largest(uint32_t a, uint32_t b) {
+  uint32_t x = perm(a, b, 0x07060302u);
+  x = max_halves(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, true));
+  x = max_halves(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, true));
+  const auto p = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  x = max_halves(p[0], p[1]);
+  const auto q = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return max_halves(q[0], q[1]);
+}
+
+// A positive binary16 number's exponent as frexp gives it; kNone of 0
+constexpr int kNone = -1000;
+__device__ __forceinline__ int exponent_of(uint32_t bits) {
+  return bits >= 0x400u ? (int)(bits >> 10) - 14 : bits ? 8 - __builtin_clz(bits) : kNone;
+}
+// Scales times 2^-e, in two steps that binary16 holds
+template <int N>
+__device__ __forceinline__ typename Dwords<N>::type scale_down(typename Dwords<N>::type d, int e) {
+  const auto power = [](int x) { return __builtin_bit_cast(half2_t, (uint32_t)(15 - x) * 0x04000400u); };
+  const half2_t f = power(e >> 1), g = power(e - (e >> 1));
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t x = d[i];  // (a bit cast of a vector's element reads element 0)
+    d[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, x) * f * g);
+  }
+  return d;
 }
 
 template <typename T, int FMT, int NB>
 __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kernel(ChunkArgs a) {
   typedef Stage<NB> S;
   typedef Cached<FMT, NB> C;
-  __shared__ __align__(16) uint8_t s_keys[S::BYTES], s_values[S::BYTES];
-  __shared__ uint32_t s_top[2][kWaves];   // largest key and value scale of each group of the tile
-  __shared__ uint64_t s_broken[kWaves];   // lanes whose part of a value row is not finite
-  __shared__ int s_bad;                   // a page number outside the cache
+  __shared__ __align__(16) uint8_t s_keys[2 * S::BYTES], s_values[2 * S::BYTES];
+  __shared__ __align__(16) uint32_t s_top[4][kWaves];  // Q8_0: the groups' largest scales, keys' in the upper half
+  __shared__ int s_bad, s_broken;  // a page number outside the cache; a value that is not finite in a tile of which some row does not see all
   const int tid = (int)threadIdx.x, lane = tid & 63, c = lane & 31, hi = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int kvh = (int)blockIdx.x % a.Hkv;
-  const Work w = find_work(a, (int)blockIdx.x / a.Hkv, false);
+  const int item = uniform((int)blockIdx.x / a.Hkv), kvh = (int)blockIdx.x - item * a.Hkv;
+  const Work w = find_work(a, item, false);
   if (w.b < 0) return;
   const Rows rt = rows_of(a, w);
   const int t_begin = w.part * w.part_tiles, t_end = min(rt.tiles, t_begin + w.part_tiles);
   const bool split = rt.tiles > w.part_tiles;
   if (w.part > 0 && t_begin >= rt.tiles) return;
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = s_broken = 0;
 
-  // the lane's row
-  const int rows = w.s.m * a.G, r = rt.r0 + 32 * wave + c;
-  const bool mine = 32 * wave < rt.count, live = r < rows;
-  const int rr = min(r, rows - 1), qi = rr / a.G, head = kvh * a.G + rr - qi * a.G;
-  const int place = qi + w.s.n - w.s.m;
+  // A lane's row; past the last row it again, which is not stored
+  const bool mine = 32 * wave < rt.count;
+  struct Row {
+    int query, head, place;
+    bool live;
+  };
+  const auto row_of = [&](int column) __attribute__((always_inline)) {
+    const int rows = w.s.m * a.G, r = rt.r0 + 32 * wave + column, rr = min(r, rows - 1), query = rr / a.G;
+    return Row{query, kvh * a.G + rr - query * a.G, query + w.s.n - w.s.m, r < rows};
+  };
+  const int place = row_of(c).place;
   const int place_first = __builtin_amdgcn_readlane(place, 0), place_last = __builtin_amdgcn_readlane(place, 31);
-  const auto seen = [&](int key) __attribute__((always_inline)) { return key <= place && (key > place - a.window || key < a.sinks); };
+  const auto seen = [&](int key) __attribute__((always_inline)) { return (key <= place) & ((key > place - a.window) | (key < a.sinks)); };
 
-  // its query, 16 places of the row's order at a time
+  // The wavefront's 16-key group of each tile: where it is in the cache, and how many of its rows are read.
+  const auto* table = (const __attribute__((address_space(4))) int32_t*)(a.table + (int64_t)w.b * a.table_stride);
+  const int page_mask = (1 << a.c.page_shift) - 1;
+  const auto tile_key = [&](int t) __attribute__((always_inline)) { return (t < rt.sink_tiles ? t : t + rt.skip) * kKeys; };
+  bool bad_page = false;
+  struct Group {
+    int64_t row;
+    int count;
+  };
+  const auto rows_seen = [&](int t) __attribute__((always_inline)) {
+    const int key0 = tile_key(t) + 16 * wave;
+    const bool none = t >= t_end || (key0 + 15 < rt.start && key0 >= rt.sink);  // no row sees any of it
+    return none ? 0 : min(max(rt.end - key0, 0), 16);
+  };
+  const auto page_of = [&](int t) __attribute__((always_inline)) { return rows_seen(t) > 0 ? table[(tile_key(t) + 16 * wave) >> a.c.page_shift] : 0; };
+  const auto group_of = [&](int t, int page) __attribute__((always_inline)) {
+    const bool out = (uint32_t)page >= (uint32_t)a.c.n_pages;
+    bad_page |= out;
+    const int64_t row = (((int64_t)(out ? 0 : page) * a.Hkv + kvh) << a.c.page_shift) + ((tile_key(t) + 16 * wave) & page_mask);
+    return Group{(int64_t)(uint32_t)uniform((int)row) | (int64_t)uniform((int)(row >> 32)) << 32, uniform(out ? 0 : rows_seen(t))};
+  };
+  const auto partly = [&](int t) __attribute__((always_inline)) {  // some row does not see some key of the tile
+    const int key0 = tile_key(t);
+    return key0 + kKeys - 1 > rt.first || (key0 <= rt.last - a.window && key0 + kKeys - 1 >= a.sinks);
+  };
+
+  // 16-bit caches: straight into LDS, 64 pieces of 16 bytes a load, in LDS order.  Rows that are not read come
+  // as zeros: a group's buffer ends behind its last one.
+  uint32_t key_from[C::Q8 ? 1 : NB], value_from[C::Q8 ? 1 : NB];
+  const uint32_t keys_at = lds_address(s_keys) + (uint32_t)(wave * 16 * S::ROW), values_at = lds_address(s_values) + (uint32_t)(wave * 16 * S::ROW);
+  if constexpr (!C::Q8) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int id = 64 * j + lane, row = id / S::PIECES, pos = id % S::PIECES;
+      key_from[j] = (uint32_t)(row * S::ROW + 16 * S::key_piece(row, pos));
+      value_from[j] = (uint32_t)(row * S::ROW + 16 * S::value_piece(row, pos));
+    }
+  }
+  const auto buffer16 = [&](const void* p, Group g) __attribute__((always_inline)) {
+    return buffer_of(reinterpret_cast<const uint8_t*>(p) + g.row * C::ROW, (uint32_t)(g.count * C::ROW));
+  };
+  const auto async_rows = [&](const void* p, Group g, const uint32_t* from, uint32_t at) __attribute__((always_inline)) {
+    const u32x4 buffer = buffer16(p, g);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) buffer_to_lds(buffer, from[j], at + 1024 * j);
+  };
+
+  // Q8_0: through registers, 4 lanes to a row, and converted into LDS a step later.
+  typedef typename Dwords<C::WORDS>::type Codes;
+  typedef typename Dwords<C::SCALES>::type Scales;
+  const int row_in = lane >> 2, seg = lane & 3;
+  const auto load_scales = [&](const void* p, Group g) __attribute__((always_inline)) {
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(reinterpret_cast<const uint16_t*>(p) + g.row * NB), 0, g.count * (2 * NB), 0x00020000);
+    if constexpr (NB % 2 == 0) {
+      return load_dwords<C::SCALES>(rsrc, 2 * NB * row_in);
+    } else {
+      Scales x;
+#pragma unroll
+      for (int i = 0; i < C::SCALES; ++i) {
+        const uint32_t u = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, 2 * (NB * row_in + 2 * i), 0, 0);
+        const uint32_t v = 2 * i + 1 < NB ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, 2 * (NB * row_in + 2 * i + 1), 0, 0) : 0u;
+        x[i] = u | v << 16;
+      }
+      return x;
+    }
+  };
+  const auto load_codes = [&](const void* p, Group g) __attribute__((always_inline)) {
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(reinterpret_cast<const uint8_t*>(p) + g.row * C::ROW), 0, g.count * C::ROW, 0x00020000);
+    return load_dwords<C::WORDS>(rsrc, row_in * C::ROW + seg * (C::ROW / 4));
+  };
+  // The largest scales of a key tile and a value tile, from all wavefronts: exponents one barrier later
+  const auto publish = [&](int slot, Scales k, Scales v) __attribute__((always_inline)) {
+    const uint32_t x = wave_largest(largest_scale<C::SCALES>(k), largest_scale<C::SCALES>(v));
+    if (lane == 0) s_top[slot][wave] = x;
+  };
+  const auto published = [&](int slot) __attribute__((always_inline)) {
+    const u32x4 x = *reinterpret_cast<const u32x4*>(s_top[slot]);
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)max_halves(max_halves(x[0], x[1]), max_halves(x[2], x[3])));
+  };
+  // Piece i of the lane's part of a row, with the scales times 2^-e, into a tile
+  const auto convert = [&](uint8_t* tile, Codes codes, Scales scales, int i, bool keys) __attribute__((always_inline)) {
+    const int row = 16 * wave + row_in, piece = NB * seg + i;
+    u32x4 y;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int pair = 4 * i + j, b = pair % NB;
+      const uint32_t two = scales[b / 2];
+      const half2_t d = __builtin_bit_cast(half2_t, two), f = half2_t{d[b & 1], d[b & 1]};
+      const uint32_t u = perm(0x64646464u, codes[pair / 2] ^ 0x80808080u, pair & 1 ? 0x04030402u : 0x04010400u);
+      y[j] = __builtin_bit_cast(uint32_t, (__builtin_bit_cast(half2_t, u) - half2_t{(_Float16)1152.0f, (_Float16)1152.0f}) * f);
+    }
+    *reinterpret_cast<u32x4*>(tile + row * S::ROW + 16 * (keys ? S::key_piece(row, piece) : S::value_piece(row, piece))) = y;
+  };
+
+  floatx16 acc[NB];
+#pragma unroll
+  for (int d = 0; d < NB; ++d)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[d][j] = 0.0f;
+  float m = -__builtin_inff(), l = 0.0f;
+  int unit = kNone;  // Q8_0: the accumulator is in units of 2^unit
+
+  // What is not finite in a value row must not meet a probability of 0 in rows that do not see it: it stays out of
+  // a tile that has keys that some row does not see, and rows that see it get it behind the last one.
+  const auto keep_finite = [&](int t, Scales d) __attribute__((always_inline)) {
+    if (partly(t)) {
+      uint32_t found = 0;
+#pragma unroll
+      for (int i = 0; i < C::SCALES; ++i) found |= not_finite<_Float16>(d[i]);
+      if (__any(found != 0)) {
+        s_broken = 1;
+#pragma unroll
+        for (int i = 0; i < C::SCALES; ++i) d[i] &= ~not_finite<_Float16>(d[i]);
+      }
+    }
+    return d;
+  };
+  // the same for a 16-bit tile that is in LDS: a wavefront its group's rows
+  const auto check_values = [&](int slot) __attribute__((always_inline)) {
+    uint8_t* p = s_values + slot * S::BYTES + wave * 16 * S::ROW + 16 * lane;
+    float z = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(p + 1024 * j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z = zero_of_pair<T>(x[i], z);
+    }
+    if (__any(z != z)) {
+      s_broken = 1;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        u32x4 x = *reinterpret_cast<const u32x4*>(p + 1024 * j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] &= ~not_finite<T>(x[i]);
+        *reinterpret_cast<u32x4*>(p + 1024 * j) = x;
+      }
+    }
+  };
+  const auto barrier = [&]() __attribute__((always_inline)) {
+    wait_reads();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  // The first tiles on their way.
+  Group g0, g1;
+  {
+    const int p0 = page_of(t_begin), p1 = page_of(t_begin + 1);
+    g0 = group_of(t_begin, p0), g1 = group_of(t_begin + 1, p1);
+  }
+  int next_page = page_of(t_begin + 2);
+  Codes k0, v0, k_codes, v_codes;  // Q8_0: the first tile, and the one that the next step converts
+  Scales k0_d, v0_d, k_scales, v_scales;
+  if constexpr (C::Q8) {
+    k0_d = load_scales(a.c.k_d, g0), v0_d = load_scales(a.c.v_d, g0), k_scales = load_scales(a.c.k_d, g1), v_scales = load_scales(a.c.v_d, g1);
+    k0 = load_codes(a.c.k, g0), v0 = load_codes(a.c.v, g0), k_codes = load_codes(a.c.k, g1), v_codes = load_codes(a.c.v, g1);
+  } else {
+    async_rows(a.c.k, g0, key_from, keys_at);
+    async_rows(a.c.v, g0, value_from, values_at);
+  }
+
+  // The row's query, 16 places of the cache's channel order at a time
   Frag qf[2 * NB];
   float to_log2 = a.scale_log2;
   {
-    const uint16_t* row = a.q + (int64_t)(w.s.q0 + qi) * a.q_t + (int64_t)head * a.q_h;
-    float top = 0.0f;
-#pragma unroll
-    for (int ks = 0; ks < 2 * NB; ++ks)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        qf[ks].v[j] = *reinterpret_cast<const uint32_t*>(row + channel_of<C::Q8, NB>(16 * ks + 8 * hi + 2 * j)) ^ a.flip;
-        if constexpr (C::Q8) {
-          float x[2];
-          unpack_pair<__bf16>(qf[ks].v[j], x);
-          top = fmaxf(top, fmaxf(fabsf(x[0]), fabsf(x[1])));
-        }
-      }
+    const Row at = row_of(c);
+    const uint16_t* row = a.q + (int64_t)(w.s.q0 + at.query) * a.q_t + (int64_t)at.head * a.q_h;
     if constexpr (C::Q8) {
+#pragma unroll
+      for (int ks = 0; ks < 2 * NB; ++ks)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) qf[ks].v[j] = *reinterpret_cast<const uint32_t*>(row + channel_of<true, NB>(16 * ks + 8 * hi + 2 * j)) ^ a.flip;
       if (a.type == NVQ_TYPE_BF16) {
         // bfloat16 into binary16 operands: scaled to 2^7 .. 2^8, exact down to 2^-32 of the largest
-        top = max_32(top);
-        const int e = top > 0.0f && top < __builtin_inff() ? 8 - __builtin_amdgcn_frexp_expf(top) : 0;
+        float largest = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < 2 * NB; ++ks)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float x[2];
+            unpack_pair<__bf16>(qf[ks].v[j], x);
+            largest = fmaxf(largest, fmaxf(fabsf(x[0]), fabsf(x[1])));
+          }
+        largest = max_32(largest);
+        const int e = largest > 0.0f && largest < __builtin_inff() ? 8 - __builtin_amdgcn_frexp_expf(largest) : 0;
 #pragma unroll
         for (int ks = 0; ks < 2 * NB; ++ks)
 #pragma unroll
@@ -257,166 +483,28 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
           }
         to_log2 = __builtin_amdgcn_ldexpf(to_log2, -e);
       }
-    }
-  }
-
-  // One 16-key group of a tile, from its page: the wavefront stages it, 4 lanes to a row.
-  const auto* table = (const __attribute__((address_space(4))) int32_t*)(a.table + (int64_t)w.b * a.table_stride);
-  const int page_mask = (1 << a.c.page_shift) - 1;
-  const auto tile_key = [&](int t) __attribute__((always_inline)) { return (t < rt.sink_tiles ? t : t + rt.skip) * kKeys; };
-  const int row_in = lane >> 2, seg = lane & 3;
-  bool bad_page = false;
-  uint32_t kw[C::WORDS], vw[C::WORDS];
-  uint16_t kd[C::SCALES], vd[C::SCALES];
-  const auto load = [&](int t) __attribute__((always_inline)) {
-    const int key0 = tile_key(t) + 16 * wave;
-    int count = min(max(rt.end - key0, 0), 16);
-    if (key0 + 15 < rt.start && key0 >= rt.sink) count = 0;  // no row sees any of it
-    const int page = count > 0 ? table[key0 >> a.c.page_shift] : 0;
-    const bool out = (uint32_t)page >= (uint32_t)a.c.n_pages;
-    bad_page |= out;
-    if (out) count = 0;
-    const int64_t row = (((int64_t)(out ? 0 : page) * a.Hkv + kvh) << a.c.page_shift) + (key0 & page_mask);
-    const auto buffer = [&](const void* p, int bytes) __attribute__((always_inline)) {
-      return __builtin_amdgcn_make_buffer_rsrc((void*)(reinterpret_cast<const uint8_t*>(p) + row * bytes), 0, count * bytes, 0x00020000);
-    };
-    const auto k = buffer(a.c.k, C::ROW), v = buffer(a.c.v, C::ROW);
-    if constexpr (C::Q8) {
-      load_dwords<C::WORDS>(k, row_in * C::ROW + seg * (C::ROW / 4), kw);
-      load_dwords<C::WORDS>(v, row_in * C::ROW + seg * (C::ROW / 4), vw);
-      const auto kds = buffer(a.c.k_d, 2 * NB), vds = buffer(a.c.v_d, 2 * NB);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        kd[b] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(kds, 2 * (row_in * NB + b), 0, 0);
-        vd[b] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(vds, 2 * (row_in * NB + b), 0, 0);
-      }
     } else {
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        load_dwords<4>(k, row_in * C::ROW + 16 * (4 * i + seg), kw + 4 * i);
-        load_dwords<4>(v, row_in * C::ROW + 16 * (4 * i + seg), vw + 4 * i);
+      for (int ks = 0; ks < 2 * NB; ++ks) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(row + 16 * ks + 8 * hi);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) qf[ks].v[j] = x[j] ^ a.flip;
       }
     }
-  };
-  // Q8_0: the exponents of the tile's largest scales, from all wavefronts
-  const auto publish = [&]() __attribute__((always_inline)) {
-    if constexpr (C::Q8) {
-      const auto top = [&](const uint16_t (&d)[C::SCALES]) __attribute__((always_inline)) {
-        uint32_t x = 0;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const uint32_t u = d[b] & 0x7FFFu;
-          x = max(x, u < 0x7C00u ? u : 0u);
-        }
-        return wave_umax(x);
-      };
-      const uint32_t k = top(kd), v = top(vd);
-      if (lane == 0) s_top[0][wave] = k, s_top[1][wave] = v;
-    }
-  };
-  const auto top_exponent = [&](int which) __attribute__((always_inline)) {  // frexp's, or a large negative for all zero
-    uint32_t x = 0;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) x = max(x, s_top[which][i]);
-    return x ? __builtin_amdgcn_frexp_expf(f16_bits_to_f32((uint16_t)x)) : -1000;
-  };
-  // A lane's part of a row into the tile.
-  const auto stage = [&](uint8_t* tile, const uint32_t (&raw)[C::WORDS], const uint16_t (&d)[C::SCALES], int e, bool keys) __attribute__((always_inline)) {
-    const int row = 16 * wave + row_in;
-    half2_t f[C::SCALES];
-    if constexpr (C::Q8) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const _Float16 x = (_Float16)__builtin_amdgcn_ldexpf(f16_bits_to_f32(d[b]), -e);
-        f[b] = half2_t{x, x};
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      u32x4 x;
-      const int piece = C::Q8 ? NB * seg + i : 4 * i + seg;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (C::Q8) {
-          const int pair = 4 * i + j;
-          const uint32_t u = perm(0x64646464u, raw[pair / 2] ^ 0x80808080u, pair & 1 ? 0x04030402u : 0x04010400u);
-          x[j] = __builtin_bit_cast(uint32_t, (__builtin_bit_cast(half2_t, u) - half2_t{(_Float16)1152.0f, (_Float16)1152.0f}) * f[pair % NB]);
-        } else {
-          x[j] = raw[4 * i + j];
-        }
-      }
-      *reinterpret_cast<u32x4*>(tile + row * S::ROW + 16 * (keys ? S::key_piece(row, piece) : S::value_piece(row, piece))) = x;
-    }
-  };
-
-  floatx16 acc[NB];
-#pragma unroll
-  for (int d = 0; d < NB; ++d)
-#pragma unroll
-    for (int j = 0; j < 16; ++j) acc[d][j] = 0.0f;
-  float m = -__builtin_inff(), l = 0.0f;
-  constexpr int kUnset = -10000;
-  int unit = kUnset;  // Q8_0: the accumulator is in units of 2^unit
+  }
 
   uint32_t key_offset[2 * NB], value_offset[NB];
 #pragma unroll
-  for (int ks = 0; ks < 2 * NB; ++ks) key_offset[ks] = (uint32_t)(c * S::ROW + 16 * S::key_piece(c, 2 * ks + hi));
+  for (int ks = 0; ks < 2 * NB; ++ks) key_offset[ks] = in_vgpr((uint32_t)(c * S::ROW + 16 * S::key_piece(c, 2 * ks + hi)));
   {
     const int jj = lane & 15, in = 4 * hi + (jj >> 2), half = (lane >> 4) & 1;
 #pragma unroll
-    for (int d = 0; d < NB; ++d) value_offset[d] = (uint32_t)(in * S::ROW + 16 * S::value_piece(in, 4 * d + 2 * half + ((jj & 3) >> 1)) + 8 * (jj & 1));
+    for (int d = 0; d < NB; ++d)
+      value_offset[d] = in_vgpr((uint32_t)(in * S::ROW + 16 * S::value_piece(in, 4 * d + 2 * half + ((jj & 3) >> 1)) + 8 * (jj & 1)));
   }
 
-  if (t_begin < t_end) load(t_begin);
-  for (int t = t_begin; t < t_end; ++t) {
-    const int key0 = tile_key(t);
-    const bool partly = key0 + kKeys - 1 > rt.first || (key0 <= rt.last - a.window && key0 + kKeys - 1 >= a.sinks);  // some row does not see some key
-    publish();
-    __syncthreads();  // everyone is done with the last tile
-    int ek = 0, ev = 0;
-    if constexpr (C::Q8) {
-      ek = top_exponent(0);
-      ek = ek > -1000 ? ek - 5 : 0;
-      const int x = top_exponent(1);
-      if (x > -1000 && (unit == kUnset || x - unit > 9)) {
-        if (unit != kUnset) {
-          const float f = __builtin_amdgcn_ldexpf(1.0f, unit - (x - 5));
-#pragma unroll
-          for (int d = 0; d < NB; ++d) acc[d] *= f;
-        }
-        unit = x - 5;
-      }
-      ev = unit == kUnset ? 0 : unit;
-    }
-    if (partly) {
-      // what is not finite in a value row must not meet a probability of 0 in rows that do not see it: it
-      // stays out of the tile, and rows that see it get it below
-      bool broken = false;
-      if constexpr (C::Q8) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) broken |= (vd[b] & 0x7C00u) == 0x7C00u;
-      } else {
-#pragma unroll
-        for (int i = 0; i < C::WORDS; ++i) broken |= not_finite<T>(vw[i]) != 0;
-      }
-      const uint64_t any = __ballot(broken);
-      if (lane == 0) s_broken[wave] = any;
-      if (any) {
-        if constexpr (C::Q8) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b) vd[b] = (vd[b] & 0x7C00u) == 0x7C00u ? 0 : vd[b];
-        } else {
-#pragma unroll
-          for (int i = 0; i < C::WORDS; ++i) vw[i] &= ~not_finite<T>(vw[i]);
-        }
-      }
-    }
-    stage(s_keys, kw, kd, ek, true);
-    stage(s_values, vw, vd, ev, false);
-    if (t + 1 < t_end) load(t + 1);
-    __syncthreads();
-    if (!mine) continue;
-
+  // Tile t in a slot, seen with scores times `factor`; between the first products, `turn` has its turns
+  const auto step = [&](int t, int slot, float factor, auto turn) __attribute__((always_inline)) {
     floatx16 s[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
@@ -426,11 +514,11 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
     for (int ks = 0; ks < 2 * NB; ++ks)
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(s_keys + key_offset[ks] + 32 * kb * S::ROW);
+        const u32x4 x = *reinterpret_cast<const u32x4*>(s_keys + slot * S::BYTES + key_offset[ks] + 32 * kb * S::ROW);
         s[kb] = mfma32<T>(Frag{x[0], x[1], x[2], x[3]}, qf[ks], s[kb]);
+        if (kb) turn(ks);
       }
-    // (not 0, which would make NaN of a masked score)
-    const float factor = C::Q8 ? fmaxf(__builtin_amdgcn_ldexpf(to_log2, ek), 1e-37f) : to_log2;
+    const int key0 = tile_key(t);
     if (key0 + kKeys - 1 > place_first || (key0 <= place_last - a.window && key0 + kKeys - 1 >= a.sinks)) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
@@ -474,40 +562,140 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
           Frag f;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const u32x2 y = read_transposed(s_values + value_offset[d] + (32 * kb + 16 * h + 8 * x) * S::ROW);
+            const u32x2 y = read_transposed(s_values + slot * S::BYTES + value_offset[d] + (32 * kb + 16 * h + 8 * x) * S::ROW);
             f.v[2 * x] = y[0], f.v[2 * x + 1] = y[1];
           }
           acc[d] = mfma32<T>(f, pf[kb][h], acc[d]);
         }
-    if (partly) {
-      for (int g = 0; g < kWaves; ++g)
-        for (uint64_t any = s_broken[g]; any;) {
-          const int row4 = __builtin_ctzll(any) >> 2, key = key0 + 16 * g + row4;
-          any &= ~(uint64_t(15) << (4 * row4));
-          const int64_t row = (((int64_t)table[key >> a.c.page_shift] * a.Hkv + kvh) << a.c.page_shift) + (key & page_mask);
-          if (!seen(key)) continue;
+  };
+  // Exponents for a tile with the largest scales x (keys' in the upper half): the keys', and the values', which is the
+  // accumulator's unit from that tile on
+  const auto key_unit = [&](uint32_t x) __attribute__((always_inline)) {
+    const int e = exponent_of(x >> 16);
+    return e == kNone ? 0 : e - 5;
+  };
+  const auto value_unit = [&](uint32_t x) __attribute__((always_inline)) {
+    const int e = exponent_of(x & 0xFFFFu);
+    return e == kNone || (unit != kNone && e - unit <= 9 && e - unit >= -3) ? unit : e - 5;
+  };
+  // base 2, of a score with the keys in units of 2^e (not 0, which would make NaN of a masked score)
+  const auto factor_of = [&](int e) __attribute__((always_inline)) { return fmaxf(__builtin_amdgcn_ldexpf(to_log2, e), 1e-37f); };
+
+  if (t_begin < t_end) {
+    float factor = 0.0f;
+    if constexpr (C::Q8) {
+      publish(2, k0_d, v0_d);
+      publish(1, k_scales, v_scales);
+      barrier();
+      const uint32_t x = published(2);
+      const int e = key_unit(x);
+      unit = value_unit(x);
+      k0_d = scale_down<C::SCALES>(k0_d, e), v0_d = scale_down<C::SCALES>(keep_finite(t_begin, v0_d), unit == kNone ? 0 : unit);
 #pragma unroll
-          for (int d = 0; d < NB; ++d)
+      for (int i = 0; i < NB; ++i) convert(s_keys, k0, k0_d, i, true);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int at = 32 * d + 8 * (j >> 2) + 4 * hi + (j & 3);
-              if constexpr (C::Q8) {
-                const uint16_t x = reinterpret_cast<const uint16_t*>(a.c.v_d)[row * NB + (at >> 1) % NB];
-                if ((x & 0x7C00u) == 0x7C00u) acc[d][j] = __builtin_nanf("");
-              } else {
-                const uint16_t x = reinterpret_cast<const uint16_t*>(a.c.v)[row * (32 * NB) + at];
-                if (not_finite<T>(x) & 0xFFFFu) acc[d][j] += (float)__builtin_bit_cast(T, x);
-              }
-            }
+      for (int i = 0; i < NB; ++i) convert(s_values, v0, v0_d, i, false);
+      factor = factor_of(e);
+    } else {
+      wait_loads<0>();
+    }
+    barrier();
+    // Step t.  16-bit: tile t + 1 goes on its way.  Q8_0: tile t + 1, in registers, is converted between the first products,
+    // and the loads of tile t + 2 begin, scales first: their largest are known to everyone one barrier later.
+    const auto pass = [&](int t, int slot) __attribute__((always_inline)) {
+      const Group g2 = group_of(t + 2, next_page);
+      next_page = page_of(t + 3);
+      uint8_t* const keys = s_keys + (slot ^ 1) * S::BYTES;
+      uint8_t* const values = s_values + (slot ^ 1) * S::BYTES;
+      if constexpr (C::Q8) {
+        const Scales k_next = load_scales(a.c.k_d, g2), v_next = load_scales(a.c.v_d, g2);
+        const uint32_t x = published(slot ^ 1);
+        const int e = key_unit(x), u = value_unit(x);
+        k_scales = scale_down<C::SCALES>(k_scales, e), v_scales = scale_down<C::SCALES>(keep_finite(t + 1, v_scales), u == kNone ? 0 : u);
+        const auto turn = [&](int j) __attribute__((always_inline)) {
+          if (j < NB)
+            convert(keys, k_codes, k_scales, j, true);
+          else
+            convert(values, v_codes, v_scales, j - NB, false);
+        };
+        if (mine) {
+          step(t, slot, factor, turn);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2 * NB; ++j) turn(j);
         }
+        if (u != unit) {
+          if (unit != kNone) {
+            const float f = __builtin_amdgcn_ldexpf(1.0f, unit - u);
+#pragma unroll
+            for (int d = 0; d < NB; ++d) acc[d] *= f;
+          }
+          unit = u;
+        }
+        factor = factor_of(e);
+        k_codes = load_codes(a.c.k, g2), v_codes = load_codes(a.c.v, g2);
+        publish(slot, k_next, v_next);
+        k_scales = k_next, v_scales = v_next;
+      } else {
+        if (partly(t)) {
+          check_values(slot);
+          barrier();
+        }
+        const u32x4 kb = buffer16(a.c.k, g1), vb = buffer16(a.c.v, g1);
+        const auto turn = [&](int j) __attribute__((always_inline)) {
+          if (j < NB)
+            buffer_to_lds(kb, key_from[j], keys_at + (slot ^ 1) * S::BYTES + 1024 * j);
+          else
+            buffer_to_lds(vb, value_from[j - NB], values_at + (slot ^ 1) * S::BYTES + 1024 * (j - NB));
+        };
+        if (mine) {
+          step(t, slot, a.scale_log2, turn);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2 * NB; ++j) turn(j);
+        }
+        wait_loads<0>();
+      }
+      g1 = g2;
+      barrier();
+    };
+    for (int t = t_begin;;) {
+      pass(t, 0);
+      if (++t >= t_end) break;
+      pass(t, 1);
+      if (++t >= t_end) break;
     }
   }
   if (bad_page) s_bad = 1;
   __syncthreads();
   if (!mine) return;
   l = sum_32(l);
+  const Row row = row_of(in_vgpr((uint32_t)lane) & 31);
+  if (s_broken) {
+    for (int t = t_begin; t < t_end; ++t)
+      for (int j = partly(t) ? 0 : kKeys; j < kKeys; ++j) {
+        const int key = tile_key(t) + j;
+        if (!(key <= row.place && (key > row.place - a.window || key < a.sinks))) continue;
+        const int page = table[key >> a.c.page_shift];
+        if ((uint32_t)page >= (uint32_t)a.c.n_pages) continue;
+        const int64_t from = (((int64_t)page * a.Hkv + kvh) << a.c.page_shift) + (key & page_mask);
+#pragma unroll
+        for (int d = 0; d < NB; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int at = 32 * d + 8 * (i >> 2) + 4 * hi + (i & 3);
+            if constexpr (C::Q8) {
+              const uint16_t x = reinterpret_cast<const uint16_t*>(a.c.v_d)[from * NB + (at >> 1) % NB];
+              if ((x & 0x7C00u) == 0x7C00u) acc[d][i] = __builtin_nanf("");
+            } else {
+              const uint16_t x = reinterpret_cast<const uint16_t*>(a.c.v)[from * (32 * NB) + at];
+              if (not_finite<T>(x) & 0xFFFFu) acc[d][i] += (float)__builtin_bit_cast(T, x);
+            }
+          }
+      }
+  }
   if (s_bad || w.s.bad) l = __builtin_nanf("");
-  if (C::Q8 && unit != kUnset) {
+  if (C::Q8 && unit != kNone) {
     const float f = __builtin_amdgcn_ldexpf(1.0f, unit);
 #pragma unroll
     for (int d = 0; d < NB; ++d) acc[d] *= f;
@@ -525,16 +713,16 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
     }
     return;
   }
-  if (!live) return;
+  if (!row.live) return;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a query that sees no key gives zeros
-  uint16_t* row = a.out + (int64_t)(w.s.q0 + qi) * a.o_t + (int64_t)head * a.o_h;
+  uint16_t* out = a.out + (int64_t)(w.s.q0 + row.query) * a.o_t + (int64_t)row.head * a.o_h;
 #pragma unroll
   for (int d = 0; d < NB; ++d)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = acc[d][2 * j] * inv, y = acc[d][2 * j + 1] * inv;
       const int at = channel_of<C::Q8, NB>(32 * d + 8 * (j >> 1) + 4 * hi + 2 * (j & 1));
-      *reinterpret_cast<uint32_t*>(row + at) = a.type == NVQ_TYPE_F16 ? pack_pair<_Float16>(x, y) : pack_pair<__bf16>(x, y);
+      *reinterpret_cast<uint32_t*>(out + at) = a.type == NVQ_TYPE_F16 ? pack_pair<_Float16>(x, y) : pack_pair<__bf16>(x, y);
     }
 }
 
@@ -544,11 +732,11 @@ __global__ __launch_bounds__(64 * kWaves) void attn_chunk_join_kernel(ChunkArgs 
   typedef Cached<FMT, NB> C;
   const int tid = (int)threadIdx.x, lane = tid & 63, c = lane & 31, hi = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int kvh = (int)blockIdx.x % a.Hkv, d = (int)blockIdx.y;
-  const Work w = find_work(a, (int)blockIdx.x / a.Hkv, true);
+  const int item = uniform((int)blockIdx.x / a.Hkv), kvh = (int)blockIdx.x - item * a.Hkv, d = (int)blockIdx.y;
+  const Work w = find_work(a, item, true);
   if (w.b < 0) return;
   const Rows rt = rows_of(a, w);
-  const int parts = (rt.tiles + w.part_tiles - 1) / w.part_tiles;
+  const int parts = uniform((rt.tiles + w.part_tiles - 1) / w.part_tiles);
   if (parts <= 1 || 32 * wave >= rt.count) return;
   floatx4 acc[4];
 #pragma unroll
@@ -582,12 +770,13 @@ __global__ __launch_bounds__(64 * kWaves) void attn_chunk_join_kernel(ChunkArgs 
 struct Bound {
   int64_t tiles;   // row tiles of a key head
   int64_t keys;    // key tiles of one
-  int64_t target;  // parts wanted
+  int64_t places;  // workgroups at once
+  int64_t target;  // parts wanted, at most
   int64_t parts;   // parts at most
   int64_t slots;   // of them of split row tiles
   int slot_waves;
 };
-Bound bound_of(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t capacity, int64_t window, int64_t sinks) {
+Bound bound_of(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity, int64_t window, int64_t sinks) {
   Bound b;
   const int64_t G = Hq / Hkv;
   b.tiles = Tq * G / kRows + B;
@@ -596,7 +785,9 @@ Bound bound_of(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t capacity,
     const int64_t seen = (sinks + kKeys - 1) / kKeys + (window + kRows - 1 + kKeys - 1) / kKeys + 1;
     b.keys = seen < b.keys ? seen : b.keys;
   }
-  b.target = kTargetGroups / Hkv < 1 ? 1 : kTargetGroups / Hkv;
+  const int64_t at_once = places((int)(D / 32)) / Hkv;
+  b.places = at_once < 1 ? 1 : at_once;
+  b.target = kRounds * b.places;
   // a sequence of `tiles` row tiles that see up to `most` key tiles is cut into tiles * ceil(most / part), and part is at
   // least sum(tiles * most) / target
   const int64_t each = (b.keys + kMinPart - 1) / kMinPart, all = b.tiles * each;
@@ -633,19 +824,19 @@ hipError_t launch_fmt(const ChunkArgs& a, int nb, const Bound& b, hipStream_t s)
 }  // namespace
 
 size_t attn_chunk_workspace(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity, int64_t window, int64_t sinks) {
-  const Bound b = bound_of(B, Tq, Hq, Hkv, capacity, window, sinks);
+  const Bound b = bound_of(B, Tq, Hq, Hkv, D, capacity, window, sinks);
   return (size_t)(b.slots * Hkv) * ((size_t)b.slot_waves * 32 * D * 4 + 2 * kRows * 4);
 }
 
-bool attn_chunk_fits(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t capacity) {
-  const Bound b = bound_of(B, Tq, Hq, Hkv, capacity, 0, 0);
+bool attn_chunk_fits(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
+  const Bound b = bound_of(B, Tq, Hq, Hkv, D, capacity, 0, 0);
   return Tq * (Hq / Hkv) < (int64_t(1) << 31) - 2 * kRows && b.tiles < (int64_t(1) << 31) / b.keys && b.parts * Hkv * (64 * kWaves) < int64_t(1) << 32;
 }
 
 hipError_t launch_attn_chunk(int fmt, int type, const void* q, void* out, const int64_t strides[4], int64_t B, int64_t Tq, int64_t Hq,
                              int64_t Hkv, int64_t D, const KvCache& c, const int32_t* table, int64_t table_stride, const int32_t* cu_q,
                              const int32_t* lengths, int window, int sinks, float scale, void* workspace, hipStream_t stream) {
-  const Bound b = bound_of(B, Tq, Hq, Hkv, table_stride << c.page_shift, window, sinks);
+  const Bound b = bound_of(B, Tq, Hq, Hkv, D, table_stride << c.page_shift, window, sinks);
   ChunkArgs a;
   a.q = (const uint16_t*)q, a.out = (uint16_t*)out;
   a.q_t = strides[0], a.q_h = strides[1], a.o_t = strides[2], a.o_h = strides[3];
@@ -662,7 +853,7 @@ hipError_t launch_attn_chunk(int fmt, int type, const void* q, void* out, const 
   a.B = (int)B, a.Hq = (int)Hq, a.Hkv = (int)Hkv, a.G = (int)(Hq / Hkv), a.Tq = (int)Tq;
   a.window = window ? window : 1 << 30, a.sinks = window ? sinks : 0;
   a.type = type;
-  a.target = (int)b.target;
+  a.places = (int)b.places;
   a.slot_waves = b.slot_waves;
   const int nb = (int)(D / 32);
   if (fmt == NVQ_KV_Q8_0) return launch_fmt<_Float16, NVQ_KV_Q8_0>(a, nb, b, stream);

@@ -918,7 +918,7 @@ nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v
 static bool chunk_shape_ok(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages, int64_t page) {
   constexpr int64_t most = int64_t(1) << 30;
   return B >= 1 && B < most && Tq >= 1 && Tq < most && Hkv >= 1 && Hkv <= 65536 && Hq >= Hkv && Hq <= 65536 && Hq % Hkv == 0 && D >= 32 && D <= 256 &&
-         D % 32 == 0 && page_ok(page) && max_pages >= 1 && max_pages < most / page && nvq::attn_chunk_fits(B, Tq, Hq, Hkv, max_pages * page);
+         D % 32 == 0 && page_ok(page) && max_pages >= 1 && max_pages < most / page && nvq::attn_chunk_fits(B, Tq, Hq, Hkv, D, max_pages * page);
 }
 
 // A window of all keys that the tables' pages can hold, or first keys that are all of them, is none.

@@ -170,7 +170,7 @@ hipError_t launch_attn_chunk(int fmt, int type, const void* q, void* out, const 
                              const int32_t* lengths, int window, int sinks, float scale, void* workspace, hipStream_t stream);
 size_t attn_chunk_workspace(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity, int64_t window, int64_t sinks);
 // Whether its tile counts fit 31 bits and its launches stay below 2^32 threads.
-bool attn_chunk_fits(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t capacity);
+bool attn_chunk_fits(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity);
 
 // Measurement probes (probe.hip): a streaming read of n16 16-byte units over `blocks`
 // blocks of 256 threads (sink: 4 words per block); the decode GEMV's weight loads
