@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kWaves = kTileWaves;
 constexpr int kRows = 32 * kWaves;  // of a workgroup
-constexpr int kMinPart = 2;  // tiles: the shortest part
+constexpr int kMinPart = 1;  // tiles: the shortest part
 // Parts for one round of workgroups over the chip, or for two where a workgroup's share of the call is more than
 // this many tiles (the last round's idle places then cost less).
 constexpr int kOneRound = 32, kRounds = 2;
@@ -97,8 +97,9 @@ struct Work {
 __device__ __forceinline__ Work find_work(const ChunkArgs& a, int want, bool join) {
   const int lane = (int)(threadIdx.x & 63);
   int total = 0, all = 0;  // key tiles of all row tiles (below 2^31: host check), and row tiles
+  const Seq head = load_seq(a, lane);
   for (int i0 = 0; i0 < a.B; i0 += 64) {
-    const Seq s = load_seq(a, i0 + lane);
+    const Seq s = i0 ? load_seq(a, i0 + lane) : head;
     total += s.tiles * s.most, all += s.tiles;
   }
   total = __builtin_amdgcn_readlane(wave_running_sum(total), 63);
@@ -111,7 +112,7 @@ __device__ __forceinline__ Work find_work(const ChunkArgs& a, int want, bool joi
   w.b = -1;
   int base = 0, slots = 0;
   for (int i0 = 0; i0 < a.B; i0 += 64) {
-    const Seq s = load_seq(a, i0 + lane);
+    const Seq s = i0 ? load_seq(a, i0 + lane) : head;
     const int parts = max(1, (s.most + most - 1) / most);
     const int taken = parts > 1 ? s.tiles * parts : 0;
     const int mine = join ? (parts > 1 ? s.tiles : 0) : s.tiles * parts;
@@ -288,6 +289,24 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
   const int place_first = __builtin_amdgcn_readlane(place, 0), place_last = __builtin_amdgcn_readlane(place, 31);
   const auto seen = [&](int key) __attribute__((always_inline)) { return (key <= place) & ((key > place - a.window) | (key < a.sinks)); };
 
+  // Its query, 16 places of the cache's channel order at a time, on the way before the keys' place is known
+  Frag qf[2 * NB];
+  {
+    const Row at = row_of(c);
+    const uint16_t* row = a.q + (int64_t)(w.s.q0 + at.query) * a.q_t + (int64_t)at.head * a.q_h;
+#pragma unroll
+    for (int ks = 0; ks < 2 * NB; ++ks) {
+      if constexpr (C::Q8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) qf[ks].v[j] = *reinterpret_cast<const uint32_t*>(row + channel_of<true, NB>(16 * ks + 8 * hi + 2 * j));
+      } else {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(row + 16 * ks + 8 * hi);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) qf[ks].v[j] = x[j];
+      }
+    }
+  }
+
   // The wavefront's 16-key group of each tile: where it is in the cache, and how many of its rows are read.
   const auto* table = (const __attribute__((address_space(4))) int32_t*)(a.table + (int64_t)w.b * a.table_stride);
   const int page_mask = (1 << a.c.page_shift) - 1;
@@ -449,49 +468,36 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
     async_rows(a.c.v, g0, value_from, values_at);
   }
 
-  // The row's query, 16 places of the cache's channel order at a time
-  Frag qf[2 * NB];
+  // bfloat16 queries into binary16 operands: scaled to 2^7 .. 2^8, exact down to 2^-32 of the largest
   float to_log2 = a.scale_log2;
-  {
-    const Row at = row_of(c);
-    const uint16_t* row = a.q + (int64_t)(w.s.q0 + at.query) * a.q_t + (int64_t)at.head * a.q_h;
-    if constexpr (C::Q8) {
+  if constexpr (C::Q8) {
+    if (a.type == NVQ_TYPE_BF16) {
+      float largest = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < 2 * NB; ++ks)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) qf[ks].v[j] = *reinterpret_cast<const uint32_t*>(row + channel_of<true, NB>(16 * ks + 8 * hi + 2 * j)) ^ a.flip;
-      if (a.type == NVQ_TYPE_BF16) {
-        // bfloat16 into binary16 operands: scaled to 2^7 .. 2^8, exact down to 2^-32 of the largest
-        float largest = 0.0f;
+        for (int j = 0; j < 4; ++j) {
+          float x[2];
+          unpack_pair<__bf16>(qf[ks].v[j], x);
+          largest = fmaxf(largest, fmaxf(fabsf(x[0]), fabsf(x[1])));
+        }
+      largest = max_32(largest);
+      const int e = largest > 0.0f && largest < __builtin_inff() ? 8 - __builtin_amdgcn_frexp_expf(largest) : 0;
 #pragma unroll
-        for (int ks = 0; ks < 2 * NB; ++ks)
+      for (int ks = 0; ks < 2 * NB; ++ks)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float x[2];
-            unpack_pair<__bf16>(qf[ks].v[j], x);
-            largest = fmaxf(largest, fmaxf(fabsf(x[0]), fabsf(x[1])));
-          }
-        largest = max_32(largest);
-        const int e = largest > 0.0f && largest < __builtin_inff() ? 8 - __builtin_amdgcn_frexp_expf(largest) : 0;
-#pragma unroll
-        for (int ks = 0; ks < 2 * NB; ++ks)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float x[2];
-            unpack_pair<__bf16>(qf[ks].v[j], x);
-            qf[ks].v[j] = pack_pair<_Float16>(__builtin_amdgcn_ldexpf(x[0], e), __builtin_amdgcn_ldexpf(x[1], e));
-          }
-        to_log2 = __builtin_amdgcn_ldexpf(to_log2, -e);
-      }
-    } else {
-#pragma unroll
-      for (int ks = 0; ks < 2 * NB; ++ks) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(row + 16 * ks + 8 * hi);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) qf[ks].v[j] = x[j] ^ a.flip;
-      }
+        for (int j = 0; j < 4; ++j) {
+          float x[2];
+          unpack_pair<__bf16>(qf[ks].v[j], x);
+          qf[ks].v[j] = pack_pair<_Float16>(__builtin_amdgcn_ldexpf(x[0], e), __builtin_amdgcn_ldexpf(x[1], e));
+        }
+      to_log2 = __builtin_amdgcn_ldexpf(to_log2, -e);
     }
   }
+#pragma unroll
+  for (int ks = 0; ks < 2 * NB; ++ks)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) qf[ks].v[j] ^= a.flip;
 
   uint32_t key_offset[2 * NB], value_offset[NB];
 #pragma unroll
@@ -659,12 +665,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
       g1 = g2;
       barrier();
     };
-    for (int t = t_begin;;) {
-      pass(t, 0);
-      if (++t >= t_end) break;
-      pass(t, 1);
-      if (++t >= t_end) break;
-    }
+    for (int t = t_begin, slot = 0; t < t_end; ++t, slot ^= 1) pass(t, slot);
   }
   if (bad_page) s_bad = 1;
   __syncthreads();
