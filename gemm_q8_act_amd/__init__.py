@@ -125,7 +125,7 @@ def lib() -> ctypes.CDLL:
                                                I64, I64, P, I64, P, F, P, P, SZ, P]),
             "nvq_attn_decode_window": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, P, I64, I64, I64, I64, I64, I64, P, P, P, P,
                                                       I64, I64, P, I64, P, F, I64, I64, P, P, SZ, P]),
-            "nvq_attn_chunk_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I64, I64, I64, I64]),
+            "nvq_attn_chunk_workspace_bytes": (SZ, [ctypes.c_int, I64, I64, I64, I64, I64, I64, I64, I64, I64]),
             "nvq_attn_chunk": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, P, P, I64, I64, I64, I64, I64, P, P, P, P, I64, I64, P, I64, P, P, F, I64, I64,
                                               P, P, SZ, P]),
             "nvq_attn_prompt": (ctypes.c_int, [ctypes.c_int, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, F,
@@ -1023,8 +1023,8 @@ _Strides4 = ctypes.c_int64 * 4
 
 
 @functools.lru_cache(maxsize=256)
-def nvq_attn_chunk_workspace_bytes(B: int, Tq: int, Hq: int, Hkv: int, D: int, max_pages: int, page: int, window: int = 0, sinks: int = 0) -> int:
-    return int(lib().nvq_attn_chunk_workspace_bytes(B, Tq, Hq, Hkv, D, max_pages, page, window, sinks))
+def nvq_attn_chunk_workspace_bytes(fmt: int, B: int, Tq: int, Hq: int, Hkv: int, D: int, max_pages: int, page: int, window: int = 0, sinks: int = 0) -> int:
+    return int(lib().nvq_attn_chunk_workspace_bytes(fmt, B, Tq, Hq, Hkv, D, max_pages, page, window, sinks))
 
 
 def nvq_attn_chunk(q, k_cache, v_cache, table, cu_q, lengths, out, k_d=None, v_d=None, window=0, sinks=0, scale=None, workspace=None,
@@ -1065,7 +1065,7 @@ def nvq_attn_chunk(q, k_cache, v_cache, table, cu_q, lengths, out, k_d=None, v_d
         _wrong_device(q, k_cache, v_cache, table, cu_q, lengths, out, k_d, v_d, workspace)
         raise ValueError("q, out, the cache, table, cu_q, lengths and workspace do not fit together")
     if workspace is None:
-        workspace = _workspace(nvq_attn_chunk_workspace_bytes(B, Tq, Hq, heads, D, max_pages, page, window, sinks), stream, q)
+        workspace = _workspace(nvq_attn_chunk_workspace_bytes(fmt, B, Tq, Hq, heads, D, max_pages, page, window, sinks), stream, q)
     wp, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = L.nvq_attn_chunk(fmt, code, q.data_ptr(), _Strides4(qs[0], qs[1], ps[0], ps[1]), B, Tq, Hq, heads, D, k_cache.data_ptr(), v_cache.data_ptr(),
                           None if fmt else k_d.data_ptr(), None if fmt else v_d.data_ptr(), n_pages, page, table.data_ptr(), max_pages,

@@ -28,6 +28,9 @@ constexpr int kMinPart = 1;  // tiles: the shortest part
 // Parts for one round of workgroups over the chip, or for two where a workgroup's share of the call is more than
 // this many tiles (the last round's idle places then cost less).
 constexpr int kOneRound = 32, kRounds = 2;
+// Q8_0 is turned into binary16 first from so many rows (query, head) a sequence on, on average, in so much workspace
+// at most.
+constexpr int64_t kExpandRows = 8 * kRows, kExpandBytes = int64_t(1) << 30;
 // Workgroups that the chip holds at once (by registers), for nb 32-blocks a row
 constexpr int places(int nb) { return 256 * (nb <= 2 ? 3 : nb <= 4 ? 2 : 1); }
 
@@ -47,6 +50,11 @@ struct ChunkArgs {
   int type;
   int places;      // workgroups at once of a key head
   int slot_waves;  // wavefronts' rows that a part's slot holds
+  // Q8_0 turned into binary16 before (kExpanded): rows [sequence][key head][tile][64] in the cache's channel order, and of
+  // each tile the powers of two that its keys (lower half) and values were divided by
+  uint16_t *keys, *values;
+  int* units;
+  int tiles;       // of a sequence there
 };
 
 // Tiles that the 128 rows of one workgroup see of n keys, at most: with a window, those of the first keys, and of
@@ -162,9 +170,11 @@ __device__ __forceinline__ Rows rows_of(const ChunkArgs& a, const Work& w) {
   return r;
 }
 
+constexpr int kExpanded = 16;
 template <int FMT, int NB>
 struct Cached {
-  static constexpr bool Q8 = FMT == NVQ_KV_Q8_0;
+  static constexpr bool Q8 = FMT == NVQ_KV_Q8_0, EXPANDED = FMT == kExpanded;
+  static constexpr bool MIXED = Q8 || EXPANDED;       // channels in the quantised order, tiles in units of a power of two
   static constexpr int ROW = Q8 ? 32 * NB : 64 * NB;  // bytes of a cache row
   static constexpr int WORDS = Q8 ? 2 * NB : 1;       // Q8_0: dwords that a lane takes of it (4 lanes to a row)
   static constexpr int SCALES = Q8 ? (NB + 1) / 2 : 1;  // its scales, two a dword
@@ -257,6 +267,38 @@ __device__ __forceinline__ typename Dwords<N>::type scale_down(typename Dwords<N
   return d;
 }
 
+// The scales of row `row_in` of a group
+template <int NB>
+__device__ __forceinline__ typename Dwords<(NB + 1) / 2>::type load_row_scales(__amdgpu_buffer_rsrc_t r, int row_in) {
+  if constexpr (NB % 2 == 0) {
+    return load_dwords<NB / 2>(r, 2 * NB * row_in);
+  } else {
+    typename Dwords<(NB + 1) / 2>::type x;
+#pragma unroll
+    for (int i = 0; i < (NB + 1) / 2; ++i) {
+      const uint32_t u = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, 2 * (NB * row_in + 2 * i), 0, 0);
+      const uint32_t v = 2 * i + 1 < NB ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, 2 * (NB * row_in + 2 * i + 1), 0, 0) : 0u;
+      x[i] = u | v << 16;
+    }
+    return x;
+  }
+}
+// Codes times scales, eight of them: piece i of a quarter of a row.  (1152 = 1024 + 128: the byte, its sign bit turned,
+// is the end of a binary16 number's mantissa)
+template <int NB>
+__device__ __forceinline__ u32x4 to_halves(typename Dwords<2 * NB>::type codes, typename Dwords<(NB + 1) / 2>::type scales, int i) {
+  u32x4 y;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int pair = 4 * i + j, b = pair % NB;
+    const uint32_t two = scales[b / 2];
+    const half2_t d = __builtin_bit_cast(half2_t, two), f = half2_t{d[b & 1], d[b & 1]};
+    const uint32_t u = perm(0x64646464u, codes[pair / 2] ^ 0x80808080u, pair & 1 ? 0x04030402u : 0x04010400u);
+    y[j] = __builtin_bit_cast(uint32_t, (__builtin_bit_cast(half2_t, u) - half2_t{(_Float16)1152.0f, (_Float16)1152.0f}) * f);
+  }
+  return y;
+}
+
 template <typename T, int FMT, int NB>
 __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kernel(ChunkArgs a) {
   typedef Stage<NB> S;
@@ -296,7 +338,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
     const uint16_t* row = a.q + (int64_t)(w.s.q0 + at.query) * a.q_t + (int64_t)at.head * a.q_h;
 #pragma unroll
     for (int ks = 0; ks < 2 * NB; ++ks) {
-      if constexpr (C::Q8) {
+      if constexpr (C::MIXED) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) qf[ks].v[j] = *reinterpret_cast<const uint32_t*>(row + channel_of<true, NB>(16 * ks + 8 * hi + 2 * j));
       } else {
@@ -321,12 +363,17 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
     const bool none = t >= t_end || (key0 + 15 < rt.start && key0 >= rt.sink);  // no row sees any of it
     return none ? 0 : min(max(rt.end - key0, 0), 16);
   };
-  const auto page_of = [&](int t) __attribute__((always_inline)) { return rows_seen(t) > 0 ? table[(tile_key(t) + 16 * wave) >> a.c.page_shift] : 0; };
+  const auto page_of = [&](int t) __attribute__((always_inline)) { return !C::EXPANDED && rows_seen(t) > 0 ? table[(tile_key(t) + 16 * wave) >> a.c.page_shift] : 0; };
+  const int64_t first_tile = C::EXPANDED ? ((int64_t)w.b * a.Hkv + kvh) * a.tiles : 0;
   const auto group_of = [&](int t, int page) __attribute__((always_inline)) {
+    const auto at = [&](int64_t row, int count) __attribute__((always_inline)) {
+      return Group{(int64_t)(uint32_t)uniform((int)row) | (int64_t)uniform((int)(row >> 32)) << 32, uniform(count)};
+    };
+    if constexpr (C::EXPANDED) return at(first_tile * kKeys + (t < t_end ? tile_key(t) : 0) + 16 * wave, rows_seen(t));
     const bool out = (uint32_t)page >= (uint32_t)a.c.n_pages;
     bad_page |= out;
     const int64_t row = (((int64_t)(out ? 0 : page) * a.Hkv + kvh) << a.c.page_shift) + ((tile_key(t) + 16 * wave) & page_mask);
-    return Group{(int64_t)(uint32_t)uniform((int)row) | (int64_t)uniform((int)(row >> 32)) << 32, uniform(out ? 0 : rows_seen(t))};
+    return at(row, out ? 0 : rows_seen(t));
   };
   const auto partly = [&](int t) __attribute__((always_inline)) {  // some row does not see some key of the tile
     const int key0 = tile_key(t);
@@ -345,6 +392,8 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
       value_from[j] = (uint32_t)(row * S::ROW + 16 * S::value_piece(row, pos));
     }
   }
+  const void* const all_keys = C::EXPANDED ? a.keys : a.c.k;
+  const void* const all_values = C::EXPANDED ? a.values : a.c.v;
   const auto buffer16 = [&](const void* p, Group g) __attribute__((always_inline)) {
     return buffer_of(reinterpret_cast<const uint8_t*>(p) + g.row * C::ROW, (uint32_t)(g.count * C::ROW));
   };
@@ -360,18 +409,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
   const int row_in = lane >> 2, seg = lane & 3;
   const auto load_scales = [&](const void* p, Group g) __attribute__((always_inline)) {
     const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(reinterpret_cast<const uint16_t*>(p) + g.row * NB), 0, g.count * (2 * NB), 0x00020000);
-    if constexpr (NB % 2 == 0) {
-      return load_dwords<C::SCALES>(rsrc, 2 * NB * row_in);
-    } else {
-      Scales x;
-#pragma unroll
-      for (int i = 0; i < C::SCALES; ++i) {
-        const uint32_t u = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, 2 * (NB * row_in + 2 * i), 0, 0);
-        const uint32_t v = 2 * i + 1 < NB ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, 2 * (NB * row_in + 2 * i + 1), 0, 0) : 0u;
-        x[i] = u | v << 16;
-      }
-      return x;
-    }
+    return load_row_scales<NB>(rsrc, row_in);
   };
   const auto load_codes = [&](const void* p, Group g) __attribute__((always_inline)) {
     const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(reinterpret_cast<const uint8_t*>(p) + g.row * C::ROW), 0, g.count * C::ROW, 0x00020000);
@@ -388,17 +426,10 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
   };
   // Piece i of the lane's part of a row, with the scales times 2^-e, into a tile
   const auto convert = [&](uint8_t* tile, Codes codes, Scales scales, int i, bool keys) __attribute__((always_inline)) {
-    const int row = 16 * wave + row_in, piece = NB * seg + i;
-    u32x4 y;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int pair = 4 * i + j, b = pair % NB;
-      const uint32_t two = scales[b / 2];
-      const half2_t d = __builtin_bit_cast(half2_t, two), f = half2_t{d[b & 1], d[b & 1]};
-      const uint32_t u = perm(0x64646464u, codes[pair / 2] ^ 0x80808080u, pair & 1 ? 0x04030402u : 0x04010400u);
-      y[j] = __builtin_bit_cast(uint32_t, (__builtin_bit_cast(half2_t, u) - half2_t{(_Float16)1152.0f, (_Float16)1152.0f}) * f);
+    if constexpr (C::Q8) {
+      const int row = 16 * wave + row_in, piece = NB * seg + i;
+      *reinterpret_cast<u32x4*>(tile + row * S::ROW + 16 * (keys ? S::key_piece(row, piece) : S::value_piece(row, piece))) = to_halves<NB>(codes, scales, i);
     }
-    *reinterpret_cast<u32x4*>(tile + row * S::ROW + 16 * (keys ? S::key_piece(row, piece) : S::value_piece(row, piece))) = y;
   };
 
   floatx16 acc[NB];
@@ -464,13 +495,13 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
     k0_d = load_scales(a.c.k_d, g0), v0_d = load_scales(a.c.v_d, g0), k_scales = load_scales(a.c.k_d, g1), v_scales = load_scales(a.c.v_d, g1);
     k0 = load_codes(a.c.k, g0), v0 = load_codes(a.c.v, g0), k_codes = load_codes(a.c.k, g1), v_codes = load_codes(a.c.v, g1);
   } else {
-    async_rows(a.c.k, g0, key_from, keys_at);
-    async_rows(a.c.v, g0, value_from, values_at);
+    async_rows(all_keys, g0, key_from, keys_at);
+    async_rows(all_values, g0, value_from, values_at);
   }
 
   // bfloat16 queries into binary16 operands: scaled to 2^7 .. 2^8, exact down to 2^-32 of the largest
   float to_log2 = a.scale_log2;
-  if constexpr (C::Q8) {
+  if constexpr (C::MIXED) {
     if (a.type == NVQ_TYPE_BF16) {
       float largest = 0.0f;
 #pragma unroll
@@ -587,6 +618,20 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
   // base 2, of a score with the keys in units of 2^e (not 0, which would make NaN of a masked score)
   const auto factor_of = [&](int e) __attribute__((always_inline)) { return fmaxf(__builtin_amdgcn_ldexpf(to_log2, e), 1e-37f); };
 
+  const auto use_unit = [&](int u) __attribute__((always_inline)) {
+    if (u != unit) {
+      if (unit != kNone) {
+        const float f = __builtin_amdgcn_ldexpf(1.0f, unit - u);
+#pragma unroll
+        for (int d = 0; d < NB; ++d) acc[d] *= f;
+      }
+      unit = u;
+    }
+  };
+  const auto* units = (const __attribute__((address_space(4))) int*)(C::EXPANDED ? a.units + first_tile : nullptr);
+  const auto unit_of = [&](int t) __attribute__((always_inline)) { return C::EXPANDED && t < t_end ? units[tile_key(t) / kKeys] : 0; };
+  int next_unit = unit_of(t_begin);
+
   if (t_begin < t_end) {
     float factor = 0.0f;
     if constexpr (C::Q8) {
@@ -630,14 +675,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
 #pragma unroll
           for (int j = 0; j < 2 * NB; ++j) turn(j);
         }
-        if (u != unit) {
-          if (unit != kNone) {
-            const float f = __builtin_amdgcn_ldexpf(1.0f, unit - u);
-#pragma unroll
-            for (int d = 0; d < NB; ++d) acc[d] *= f;
-          }
-          unit = u;
-        }
+        use_unit(u);
         factor = factor_of(e);
         k_codes = load_codes(a.c.k, g2), v_codes = load_codes(a.c.v, g2);
         publish(slot, k_next, v_next);
@@ -647,15 +685,21 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
           check_values(slot);
           barrier();
         }
-        const u32x4 kb = buffer16(a.c.k, g1), vb = buffer16(a.c.v, g1);
+        const u32x4 kb = buffer16(all_keys, g1), vb = buffer16(all_values, g1);
         const auto turn = [&](int j) __attribute__((always_inline)) {
           if (j < NB)
             buffer_to_lds(kb, key_from[j], keys_at + (slot ^ 1) * S::BYTES + 1024 * j);
           else
             buffer_to_lds(vb, value_from[j - NB], values_at + (slot ^ 1) * S::BYTES + 1024 * (j - NB));
         };
+        float f = a.scale_log2;
+        if constexpr (C::EXPANDED) {
+          f = factor_of((int16_t)next_unit);
+          use_unit(next_unit >> 16);
+          next_unit = unit_of(t + 1);
+        }
         if (mine) {
-          step(t, slot, a.scale_log2, turn);
+          step(t, slot, f, turn);
         } else {
 #pragma unroll
           for (int j = 0; j < 2 * NB; ++j) turn(j);
@@ -677,9 +721,9 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
       for (int j = partly(t) ? 0 : kKeys; j < kKeys; ++j) {
         const int key = tile_key(t) + j;
         if (!(key <= row.place && (key > row.place - a.window || key < a.sinks))) continue;
-        const int page = table[key >> a.c.page_shift];
+        const int page = C::EXPANDED ? 0 : table[key >> a.c.page_shift];
         if ((uint32_t)page >= (uint32_t)a.c.n_pages) continue;
-        const int64_t from = (((int64_t)page * a.Hkv + kvh) << a.c.page_shift) + (key & page_mask);
+        const int64_t from = C::EXPANDED ? first_tile * kKeys + key : (((int64_t)page * a.Hkv + kvh) << a.c.page_shift) + (key & page_mask);
 #pragma unroll
         for (int d = 0; d < NB; ++d)
 #pragma unroll
@@ -689,14 +733,14 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
               const uint16_t x = reinterpret_cast<const uint16_t*>(a.c.v_d)[from * NB + (at >> 1) % NB];
               if ((x & 0x7C00u) == 0x7C00u) acc[d][i] = __builtin_nanf("");
             } else {
-              const uint16_t x = reinterpret_cast<const uint16_t*>(a.c.v)[from * (32 * NB) + at];
+              const uint16_t x = reinterpret_cast<const uint16_t*>(all_values)[from * (32 * NB) + at];
               if (not_finite<T>(x) & 0xFFFFu) acc[d][i] += (float)__builtin_bit_cast(T, x);
             }
           }
       }
   }
   if (s_bad || w.s.bad) l = __builtin_nanf("");
-  if (C::Q8 && unit != kNone) {
+  if (C::MIXED && unit != kNone) {
     const float f = __builtin_amdgcn_ldexpf(1.0f, unit);
 #pragma unroll
     for (int d = 0; d < NB; ++d) acc[d] *= f;
@@ -722,9 +766,63 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = acc[d][2 * j] * inv, y = acc[d][2 * j + 1] * inv;
-      const int at = channel_of<C::Q8, NB>(32 * d + 8 * (j >> 1) + 4 * hi + 2 * (j & 1));
+      const int at = channel_of<C::MIXED, NB>(32 * d + 8 * (j >> 1) + 4 * hi + 2 * (j & 1));
       *reinterpret_cast<uint32_t*>(out + at) = a.type == NVQ_TYPE_F16 ? pack_pair<_Float16>(x, y) : pack_pair<__bf16>(x, y);
     }
+}
+
+// Q8_0 into binary16, tile blockIdx.x of key head and sequence blockIdx.y, where a sequence has so many row tiles
+// that converting each tile once and reading twice the bytes costs less than converting it in every one of
+// them.  A page number outside the cache makes NaN of its keys.
+template <int NB>
+__global__ __launch_bounds__(64 * kWaves) void attn_chunk_expand_kernel(ChunkArgs a) {
+  typedef Cached<NVQ_KV_Q8_0, NB> C;
+  __shared__ uint32_t s_top[kWaves];
+  const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int b = uniform((int)blockIdx.y / a.Hkv), kvh = (int)blockIdx.y - b * a.Hkv;
+  const Seq s = load_seq(a, b);
+  const int n = uniform(s.n), m = uniform(s.m);
+  const int start = max(n - m - a.window + 1, 0);  // of the first query's window
+  const auto wanted = [&](int key, int count) { return m > 0 && key < n && (key + count > start || key < a.sinks); };
+  const int tile0 = (int)blockIdx.x * kKeys, key0 = tile0 + 16 * wave;
+  if (!wanted(tile0, kKeys)) return;
+  int page = 0, count = 0;
+  if (wanted(key0, 16)) {
+    page = uniform(a.table[(int64_t)b * a.table_stride + (key0 >> a.c.page_shift)]);
+    count = min(n - key0, 16);
+  }
+  const bool out = (uint32_t)page >= (uint32_t)a.c.n_pages;
+  const int64_t from = (((int64_t)(out ? 0 : page) * a.Hkv + kvh) << a.c.page_shift) + (key0 & ((1 << a.c.page_shift) - 1));
+  const int rows = out ? 0 : count, row_in = lane >> 2, seg = lane & 3;
+  const auto buffer = [&](const void* p, int bytes) __attribute__((always_inline)) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(reinterpret_cast<const uint8_t*>(p) + from * bytes), 0, rows * bytes, 0x00020000);
+  };
+  typename Dwords<C::WORDS>::type codes[2];
+  typename Dwords<C::SCALES>::type d[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    codes[x] = load_dwords<C::WORDS>(buffer(x ? a.c.v : a.c.k, C::ROW), row_in * C::ROW + seg * (C::ROW / 4));
+    d[x] = load_row_scales<NB>(buffer(x ? a.c.v_d : a.c.k_d, 2 * NB), row_in);
+  }
+  const uint32_t mine = wave_largest(largest_scale<C::SCALES>(d[0]), largest_scale<C::SCALES>(d[1]));
+  if (lane == 0) s_top[wave] = mine;
+  __syncthreads();
+  const uint32_t top = (uint32_t)uniform((int)max_halves(max_halves(s_top[0], s_top[1]), max_halves(s_top[2], s_top[3])));
+  // the largest scale of the keys in 2^4 .. 2^5; of the values in 2^1 .. 2^9, so that most tiles have one power
+  const int ek = exponent_of(top >> 16), ev = exponent_of(top & 0xFFFFu);
+  const int e[2] = {ek == kNone ? 0 : ek - 5, ev == kNone ? 0 : ((ev - 2) >> 3) << 3};
+  const int64_t tile = (int64_t)blockIdx.y * a.tiles + blockIdx.x;
+  if (threadIdx.x == 0) a.units[tile] = (e[0] & 0xFFFF) | e[1] << 16;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const auto scales = scale_down<C::SCALES>(d[x], e[x]);
+    u32x4* const dst = reinterpret_cast<u32x4*>((x ? a.values : a.keys) + (tile * kKeys + 16 * wave + row_in) * (32 * NB)) + NB * seg;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const u32x4 y = to_halves<NB>(codes[x], scales, i);
+      dst[i] = x == 0 && out ? u32x4{~0u, ~0u, ~0u, ~0u} : y;
+    }
+  }
 }
 
 // Joins the parts of one row tile of a key head in their order: a workgroup takes 32 channels of its rows.
@@ -762,7 +860,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_chunk_join_kernel(ChunkArgs 
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float x = acc[j >> 1][2 * (j & 1)] * inv, y = acc[j >> 1][2 * (j & 1) + 1] * inv;
-    const int at = channel_of<C::Q8, NB>(32 * d + 8 * (j >> 1) + 4 * hi + 2 * (j & 1));
+    const int at = channel_of<C::MIXED, NB>(32 * d + 8 * (j >> 1) + 4 * hi + 2 * (j & 1));
     *reinterpret_cast<uint32_t*>(row + at) = a.type == NVQ_TYPE_F16 ? pack_pair<_Float16>(x, y) : pack_pair<__bf16>(x, y);
   }
 }
@@ -776,8 +874,9 @@ struct Bound {
   int64_t parts;   // parts at most
   int64_t slots;   // of them of split row tiles
   int slot_waves;
+  int64_t expanded;  // Q8_0: key tiles of a sequence, turned into binary16 first; 0: not
 };
-Bound bound_of(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity, int64_t window, int64_t sinks) {
+Bound bound_of(int fmt, int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity, int64_t window, int64_t sinks) {
   Bound b;
   const int64_t G = Hq / Hkv;
   b.tiles = Tq * G / kRows + B;
@@ -796,11 +895,21 @@ Bound bound_of(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_
   b.slots = each <= 1 ? 0 : all < 2 * b.target ? all : 2 * b.target;
   const int64_t rows = Tq * G < kRows ? Tq * G : kRows;
   b.slot_waves = (int)((rows + 31) / 32);
+  const int64_t tiles = (capacity + kKeys - 1) / kKeys;
+  const bool expand = fmt == NVQ_KV_Q8_0 && Tq * G >= B * kExpandRows && tiles <= kExpandBytes / (B * Hkv) / (kKeys * D * 4) && B * Hkv < 65536;
+  b.expanded = expand ? tiles : 0;
   return b;
 }
 
+size_t partial_bytes(const Bound& b, int64_t Hkv, int64_t D) { return (size_t)(b.slots * Hkv) * ((size_t)b.slot_waves * 32 * D * 4 + 2 * kRows * 4); }
+
 template <typename T, int FMT, int NB>
 hipError_t launch_nb(const ChunkArgs& a, const Bound& b, hipStream_t s) {
+  if constexpr (FMT == kExpanded) {
+    hipLaunchKernelGGL((attn_chunk_expand_kernel<NB>), dim3((unsigned)b.expanded, (unsigned)(a.B * a.Hkv)), dim3(64 * kWaves), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL((attn_chunk_kernel<T, FMT, NB>), dim3((unsigned)(b.parts * a.Hkv)), dim3(64 * kWaves), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || b.slots == 0) return e;
@@ -824,20 +933,20 @@ hipError_t launch_fmt(const ChunkArgs& a, int nb, const Bound& b, hipStream_t s)
 
 }  // namespace
 
-size_t attn_chunk_workspace(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity, int64_t window, int64_t sinks) {
-  const Bound b = bound_of(B, Tq, Hq, Hkv, D, capacity, window, sinks);
-  return (size_t)(b.slots * Hkv) * ((size_t)b.slot_waves * 32 * D * 4 + 2 * kRows * 4);
+size_t attn_chunk_workspace(int fmt, int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity, int64_t window, int64_t sinks) {
+  const Bound b = bound_of(fmt, B, Tq, Hq, Hkv, D, capacity, window, sinks);
+  return partial_bytes(b, Hkv, D) + (size_t)(B * Hkv * b.expanded) * (size_t)(kKeys * D * 4 + 16);
 }
 
 bool attn_chunk_fits(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity) {
-  const Bound b = bound_of(B, Tq, Hq, Hkv, D, capacity, 0, 0);
+  const Bound b = bound_of(NVQ_KV_F16, B, Tq, Hq, Hkv, D, capacity, 0, 0);
   return Tq * (Hq / Hkv) < (int64_t(1) << 31) - 2 * kRows && b.tiles < (int64_t(1) << 31) / b.keys && b.parts * Hkv * (64 * kWaves) < int64_t(1) << 32;
 }
 
 hipError_t launch_attn_chunk(int fmt, int type, const void* q, void* out, const int64_t strides[4], int64_t B, int64_t Tq, int64_t Hq,
                              int64_t Hkv, int64_t D, const KvCache& c, const int32_t* table, int64_t table_stride, const int32_t* cu_q,
                              const int32_t* lengths, int window, int sinks, float scale, void* workspace, hipStream_t stream) {
-  const Bound b = bound_of(B, Tq, Hq, Hkv, D, table_stride << c.page_shift, window, sinks);
+  const Bound b = bound_of(fmt, B, Tq, Hq, Hkv, D, table_stride << c.page_shift, window, sinks);
   ChunkArgs a;
   a.q = (const uint16_t*)q, a.out = (uint16_t*)out;
   a.q_t = strides[0], a.q_h = strides[1], a.o_t = strides[2], a.o_h = strides[3];
@@ -856,7 +965,12 @@ hipError_t launch_attn_chunk(int fmt, int type, const void* q, void* out, const 
   a.type = type;
   a.places = (int)b.places;
   a.slot_waves = b.slot_waves;
+  a.tiles = (int)b.expanded;
+  a.keys = (uint16_t*)((uint8_t*)workspace + partial_bytes(b, Hkv, D));
+  a.values = a.keys + B * Hkv * b.expanded * kKeys * D;
+  a.units = (int*)(a.values + B * Hkv * b.expanded * kKeys * D);
   const int nb = (int)(D / 32);
+  if (b.expanded) return launch_fmt<_Float16, kExpanded>(a, nb, b, stream);
   if (fmt == NVQ_KV_Q8_0) return launch_fmt<_Float16, NVQ_KV_Q8_0>(a, nb, b, stream);
   if (fmt == NVQ_KV_F16) return launch_fmt<_Float16, NVQ_KV_F16>(a, nb, b, stream);
   return launch_fmt<__bf16, NVQ_KV_BF16>(a, nb, b, stream);

@@ -924,10 +924,10 @@ static bool chunk_shape_ok(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64
 // A window of all keys that the tables' pages can hold, or first keys that are all of them, is none.
 static int64_t chunk_window(int64_t keys, int64_t window, int64_t sinks) { return window >= keys || sinks >= keys ? 0 : window; }
 
-size_t nvq_attn_chunk_workspace_bytes(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages, int64_t page,
+size_t nvq_attn_chunk_workspace_bytes(int fmt, int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages, int64_t page,
                                       int64_t window, int64_t sinks) {
-  if (!chunk_shape_ok(B, Tq, Hq, Hkv, D, max_pages, page) || window < 0 || sinks < 0) return 0;
-  return nvq::attn_chunk_workspace(B, Tq, Hq, Hkv, D, max_pages * page, chunk_window(max_pages * page, window, sinks), sinks);
+  if (!chunk_shape_ok(B, Tq, Hq, Hkv, D, max_pages, page) || window < 0 || sinks < 0 || fmt < NVQ_KV_Q8_0 || fmt > NVQ_KV_BF16) return 0;
+  return nvq::attn_chunk_workspace(fmt, B, Tq, Hq, Hkv, D, max_pages * page, chunk_window(max_pages * page, window, sinks), sinks);
 }
 
 nvq_status nvq_attn_chunk(int fmt, int type, const void* q, const int64_t* strides, int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv,
@@ -955,7 +955,7 @@ nvq_status nvq_attn_chunk(int fmt, int type, const void* q, const int64_t* strid
   if (!aligned(table, 4) || !aligned(cu_q, 4) || !aligned(lengths, 4)) return fail(NVQ_ERR_ALIGN, "%s: table, cu_q and lengths must be 4-byte aligned", who);
   const int64_t keys = max_pages * page;
   window = chunk_window(keys, window, sinks);
-  const size_t need = nvq::attn_chunk_workspace(B, Tq, Hq, Hkv, D, keys, window, sinks);
+  const size_t need = nvq::attn_chunk_workspace(fmt, B, Tq, Hq, Hkv, D, keys, window, sinks);
   if (need > 0 && (!workspace || ws_bytes < need)) return fail(NVQ_ERR_WORKSPACE, "%s: workspace of %zu bytes required, got %zu", who, need, workspace ? ws_bytes : (size_t)0);
   if (need > 0 && !aligned(workspace, 16)) return fail(NVQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", who);
   NVQ_TRY(check_device());

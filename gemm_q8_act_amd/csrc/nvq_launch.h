@@ -168,7 +168,7 @@ hipError_t launch_attn_prompt(int type, const void* q, const void* k, const void
 hipError_t launch_attn_chunk(int fmt, int type, const void* q, void* out, const int64_t strides[4], int64_t B, int64_t Tq, int64_t Hq,
                              int64_t Hkv, int64_t D, const KvCache& c, const int32_t* table, int64_t table_stride, const int32_t* cu_q,
                              const int32_t* lengths, int window, int sinks, float scale, void* workspace, hipStream_t stream);
-size_t attn_chunk_workspace(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity, int64_t window, int64_t sinks);
+size_t attn_chunk_workspace(int fmt, int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity, int64_t window, int64_t sinks);
 // Whether its tile counts fit 31 bits and its launches stay below 2^32 threads.
 bool attn_chunk_fits(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t capacity);
 

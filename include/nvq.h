@@ -610,9 +610,10 @@ nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v
  * Q8_0 in its 32-channel block) of the queries that see it, in a key row in all of theirs.  out overlaps none of
  * the inputs.
  * workspace: device, at least nvq_attn_chunk_workspace_bytes, contents irrelevant, overwritten; NULL when that
- * is 0.  Calls that share it must not overlap in time.  The bytes of more tokens, sequences or pages, or of no
- * window, are enough for fewer, or for a window. */
-size_t nvq_attn_chunk_workspace_bytes(int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages,
+ * is 0.  Calls that share it must not overlap in time.  The bytes are those of a call's own shape: Q8_0 rows
+ * are turned into binary16 there first, once for the call, where there are many queries to a sequence
+ * (Tq * Hq/Hkv >= 1024 * B, B * Hkv < 65536, and up to 1 GiB of it), so that fewer of them, or more sequences, can need more or less. */
+size_t nvq_attn_chunk_workspace_bytes(int fmt, int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages,
                                       int64_t page, int64_t window, int64_t sinks);
 nvq_status nvq_attn_chunk(int fmt, int type, const void* q, const int64_t* strides, int64_t B, int64_t Tq, int64_t Hq,
                           int64_t Hkv, int64_t D, const void* k_cache, const void* v_cache, const uint16_t* k_d,

@@ -225,7 +225,7 @@ def test_deterministic_captured_and_on_another_stream():
     call(c, x, new, out=out, cu=cu, stream=s.cuda_stream)
     s.synchronize()
     assert torch.equal(out, want)
-    need = nvq.nvq_attn_chunk_workspace_bytes(3, 231, 4, 2, 128, c.max_pages, 64)
+    need = nvq.nvq_attn_chunk_workspace_bytes(nvq.NVQ_KV_Q8_0, 3, 231, 4, 2, 128, c.max_pages, 64)
     ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
     with pytest.raises(nvq.NvqError, match="workspace"):
         call(c, x, new, workspace=ws[:need - 16])

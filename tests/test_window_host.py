@@ -55,17 +55,18 @@ def test_nothing_to_do_is_ok():
 
 def test_workspaces():
     ws = nvq.nvq_attn_chunk_workspace_bytes
-    assert ws(1, 16, 40, 8, 128, 1, 64) == 0 and ws(0, 16, 40, 8, 128, 8, 64) == 0 and ws(1, 16, 41, 8, 128, 8, 64) == 0
-    assert ws(1, 1, 40, 8, 128, 1024, 64) > 0 and ws(1, 1, 40, 8, 128, 1024, 64, -1) == 0
-    # what the header promises: the bytes of more are enough for fewer, and those of no window for any
-    sizes = [(B, T, pages, w, s) for B in (1, 3, 64) for T in (1, 7, 26, 600) for pages in (2, 9, 300) for w in (0, 1, 100, 5000) for s in (0, 4, 300)]
-    of = {x: ws(x[0], x[1], 40, 8, 128, x[2], 64, x[3], x[4]) for x in sizes}
-    for (B, T, pages, w, s), n in of.items():
-        assert n <= of[(64, 600, 300, 0, 0)] and n <= of[(B, T, pages, 0, 0)]
-        for x in ((3, T, pages, w, s), (B, 600, pages, w, s), (B, T, 300, w, s)):
-            if B <= x[0]:
-                assert n <= of[x], ((B, T, pages, w, s), x)
-    assert max(of.values()) < 140 << 20
+    q8, f16 = nvq.NVQ_KV_Q8_0, nvq.NVQ_KV_F16
+    assert ws(f16, 1, 16, 40, 8, 128, 1, 64) == 0 and ws(f16, 0, 16, 40, 8, 128, 8, 64) == 0 and ws(f16, 1, 16, 41, 8, 128, 8, 64) == 0
+    assert ws(f16, 1, 1, 40, 8, 128, 1024, 64) > 0 and ws(f16, 1, 1, 40, 8, 128, 1024, 64, -1) == 0 and ws(9, 1, 1, 40, 8, 128, 1024, 64) == 0
+    # partial results: no more than the parts of 2048 workgroups, 128 rows of float32 each
+    for B, T, pages, w, s in ((b, t, p, w, s) for b in (1, 3, 64) for t in (1, 7, 26, 600) for p in (2, 9, 300) for w in (0, 1, 100, 5000) for s in (0, 4, 300)):
+        n = ws(f16, B, T, 40, 8, 128, pages, 64, w, s)
+        assert 0 <= n <= 2048 * (128 * 128 * 4 + 1024) and ws(q8, B, T, 40, 8, 128, pages, 64, w, s) >= n
+    # Q8_0 turned into binary16 first: keys and values of 64-key tiles, and 16 bytes a tile, from 1024 rows a sequence on
+    one = 64 * 128 * 4 + 16
+    for B, T, pages, want in ((1, 204, 300, 0), (1, 205, 300, 300), (2, 409, 300, 0), (2, 410, 300, 600), (1, 4096, 4096, 4096), (1, 4096, 4097, 0), (9000, 9000 * 205, 1, 0)):
+        more = ws(q8, B, T, 40, 8, 128, pages, 64) - ws(f16, B, T, 40, 8, 128, pages, 64)
+        assert more == 8 * want * one, (B, T, pages)
 
 
 def test_binding_refusals():
