@@ -2,12 +2,18 @@
 the paged Q8_0 key-value cache and both attention operators between them.
 
   python examples/attention_layer.py [--prompt 2048] [--steps 32] [--hidden 5120] [--heads 40] [--kv-heads 8]
+                                     [--rotary [--window 1024 --sinks 4]]
 
 A prompt goes through the tiled products and nvq_attn_prompt, its keys and values into the cache;
 a second piece of the same prompt attends to the first one's rows, read back from the cache; then
 tokens are decoded one at a time: fused quantisation + GEMV, nvq_kv_write, nvq_attn_decode, fused
-GEMV.  Weights are random (no checkpoint is read); position embeddings, which belong between
-the QKV product and the cache, are left out.
+GEMV.  Weights are random (no checkpoint is read).
+
+That layer has no position embeddings.  --rotary takes the layer that has: between the QKV product and
+the attention one launch norms the query and key heads, turns them by their positions and writes keys and
+values to the cache (nvq_rope_kv_write); a piece of the prompt attends straight over the cache
+(nvq_attn_chunk), and so does a token (nvq_attn_decode_window), over the last --window keys and the first
+--sinks if given.
 """
 import argparse
 import os
@@ -106,6 +112,49 @@ class AttentionLayer:
         return out
 
 
+class RotaryLayer(AttentionLayer):
+    """The layer with normed and turned heads, attending over a window and the first keys (window 0: over all)."""
+
+    def __init__(self, hidden, heads, kv_heads, head_dim, max_tokens, page=64, seed=0, window=0, sinks=0, base=10000.0):
+        super().__init__(hidden, heads, kv_heads, head_dim, max_tokens, page, seed)
+        self.seen = dict(window=window, sinks=sinks)
+        rng = np.random.Generator(np.random.PCG64(seed + 3))
+        self.norms = [torch.from_numpy((1 + rng.standard_normal(head_dim) / 4).astype(np.float32)).cuda() for _ in "qk"]
+        self.turns = torch.from_numpy(nvq.nvq_rope_table(self.max_tokens, head_dim, base)).cuda()
+
+    def _append(self, y, dtype):
+        """Rows y of the QKV product are the next tokens: keys and values into the cache, queries normed and turned."""
+        M, first = y.shape[0], self.n
+        q, k, v = self._split(y)
+        out = torch.empty((M, self.heads, self.head_dim), dtype=dtype, device="cuda")
+        positions = torch.arange(first, first + M, dtype=torch.int32, device="cuda")
+        nvq.nvq_rope_kv_write(q, k, v, self.turns, positions, self._slots(first, M), out, *self.codes, *self.scales,
+                              q_weight=self.norms[0], k_weight=self.norms[1])
+        self.n += M
+        self.length.fill_(self.n)
+        return out
+
+    def prompt(self, x):
+        M = x.shape[0]
+        self._room(M)
+        q = self._append(self._product(self.w_qkv, self.s_qkv, x, self.rows), torch.bfloat16)
+        cu_q = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+        a = torch.empty_like(q)
+        nvq.nvq_attn_chunk(q, *self.codes, self.table, cu_q, self.length, a, *self.scales, **self.seen)
+        return self._product(self.w_o, self.s_o, a.flatten(1).float(), self.hidden)
+
+    def step(self, x):
+        self._room(1)
+        y = torch.empty((1, self.rows), dtype=torch.float32, device="cuda")
+        nvq.nvq_gemv_nvfp4_fused(self.w_qkv, self.s_qkv, x, y)
+        q = self._append(y, torch.float32)
+        a = torch.empty_like(q)
+        nvq.nvq_attn_decode_window(q, *self.codes, self.table, self.length, a, *self.scales, **self.seen, workspace=self.workspace)
+        out = torch.empty((1, self.hidden), dtype=torch.float32, device="cuda")
+        nvq.nvq_gemv_nvfp4_fused(self.w_o, self.s_o, a.flatten(1), out)
+        return out
+
+
 def main():
     p = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     p.add_argument("--prompt", type=int, default=2048)
@@ -114,10 +163,16 @@ def main():
     p.add_argument("--heads", type=int, default=40)
     p.add_argument("--kv-heads", type=int, default=8)
     p.add_argument("--head-dim", type=int, default=128)
+    p.add_argument("--rotary", action="store_true", help="the layer with normed and turned heads")
+    p.add_argument("--window", type=int, default=0, help="keys that a token sees (0: all)")
+    p.add_argument("--sinks", type=int, default=0, help="first keys that it sees besides")
     a = p.parse_args()
     if a.prompt < 2 or a.steps < 1:
         p.error("a prompt of two tokens or more (it goes in two pieces) and a step or more")
-    layer = AttentionLayer(a.hidden, a.heads, a.kv_heads, a.head_dim, a.prompt + a.steps + 1)
+    if min(a.window, a.sinks) < 0 or (a.window or a.sinks) and not a.rotary:
+        p.error("--window and --sinks go with --rotary and are not negative")
+    kind, more = (RotaryLayer, dict(window=a.window, sinks=a.sinks)) if a.rotary else (AttentionLayer, {})
+    layer = kind(a.hidden, a.heads, a.kv_heads, a.head_dim, a.prompt + a.steps + 1, **more)
     x = torch.from_numpy(synth.activations(a.prompt + a.steps, a.hidden, 3)).cuda()
     half = a.prompt // 2
     for name, run in (("first half of the prompt", lambda: layer.prompt(x[:half])), ("second half", lambda: layer.prompt(x[half:a.prompt])),
