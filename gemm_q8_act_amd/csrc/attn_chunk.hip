@@ -51,6 +51,7 @@ struct ChunkArgs {
   int type;
   int places;      // workgroups at once of a key head
   int slot_waves;  // wavefronts' rows that a part's slot holds
+  int slots;       // that there are
   // Q8_0 turned into binary16 before (kExpanded): rows [sequence][key head][tile][64] in the cache's channel order, and of
   // each tile the powers of two that its keys (lower half) and values were divided by
   uint16_t *keys, *values;
@@ -139,6 +140,8 @@ __device__ __forceinline__ Work find_work(const ChunkArgs& a, int want, bool joi
       w.part = join ? 0 : at - turn * w.parts;
       w.tile = w.s.tiles - 1 - turn;
       w.slot = w.parts > 1 ? slots + of(incl_slots) - of(taken) + turn * w.parts + w.part : -1;
+      // (only offsets that do not ascend make more of them than there is room for)
+      if (w.slot + (join ? w.parts : 1) > a.slots) w.b = -1;
       return w;
     }
     base += __builtin_amdgcn_readlane(incl, 63);
@@ -622,7 +625,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
   };
   const auto value_unit = [&](uint32_t x) __attribute__((always_inline)) {
     const int e = exponent_of(x & 0xFFFFu);
-    return e == kNone || (unit != kNone && e - unit <= 9 && e - unit >= -3) ? unit : e - 5;
+    return e == kNone || (unit != kNone && e - unit <= 9 && e - unit >= 2) ? unit : e - 5;
   };
   // base 2, of a score with the keys in units of 2^e (not 0, which would make NaN of a masked score)
   const auto factor_of = [&](int e) __attribute__((always_inline)) { return fmaxf(__builtin_amdgcn_ldexpf(to_log2, e), 1e-37f); };
@@ -817,9 +820,10 @@ __global__ __launch_bounds__(64 * kWaves) void attn_chunk_expand_kernel(ChunkArg
   if (lane == 0) s_top[wave] = mine;
   __syncthreads();
   const uint32_t top = (uint32_t)uniform((int)max_halves(max_halves(s_top[0], s_top[1]), max_halves(s_top[2], s_top[3])));
-  // the largest scale of the keys in 2^4 .. 2^5; of the values in 2^1 .. 2^9, so that most tiles have one power
+  // the largest scale of the keys in 2^4 .. 2^5; of the values in 2^1 .. 2^9, so that most tiles have one power (or 1,
+  // where all are 0 or the smallest there is)
   const int ek = exponent_of(top >> 16), ev = exponent_of(top & 0xFFFFu);
-  const int e[2] = {ek == kNone ? 0 : ek - 5, ev == kNone ? 0 : ((ev - 2) >> 3) << 3};
+  const int e[2] = {ek == kNone ? 0 : ek - 5, ev == kNone ? 0 : max(((ev - 2) >> 3) << 3, -24)};
   const int64_t tile = (int64_t)blockIdx.y * a.tiles + blockIdx.x;
   if (threadIdx.x == 0) a.units[tile] = (e[0] & 0xFFFF) | e[1] << 16;
 #pragma unroll
@@ -974,6 +978,7 @@ hipError_t launch_attn_chunk(int fmt, int type, const void* q, void* out, const 
   a.type = type;
   a.places = (int)b.places;
   a.slot_waves = b.slot_waves;
+  a.slots = (int)b.slots;
   a.tiles = (int)b.expanded;
   a.keys = (uint16_t*)((uint8_t*)workspace + partial_bytes(b, Hkv, D));
   a.values = a.keys + B * Hkv * b.expanded * kKeys * D;

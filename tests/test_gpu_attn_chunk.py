@@ -279,3 +279,23 @@ def test_rows_past_32_bit_offsets():
     nvq.nvq_attn_chunk(q, kc, vc, table, cu, lens, a, kd, vd)
     nvq.nvq_attn_chunk(q, *small[:2], torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"), cu, lens, b, *small[2:])
     assert torch.equal(a, b) and float(a.float().abs().max()) > 0
+
+
+def test_offsets_that_do_not_ascend_write_nothing_outside():
+    """4096 sequences that each claim all 8192 queries: 2^32 key tiles in all, which the work's plan does not count.  What is
+    computed is anybody's; the workspace's neighbour and the rows behind are left alone."""
+    torch = torch_dev()
+    B, Tq, D, page, pages = 4096, 8192, 32, 65536, 64
+    say("chunk offsets that do not ascend")
+    kc, vc = (torch.zeros((1, 1, page, D), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    table = torch.zeros((B, pages), dtype=torch.int32, device="cuda")
+    lengths = torch.full((B,), page * pages - 1, dtype=torch.int32, device="cuda")
+    cu = (torch.arange(B + 1, device="cuda") % 2 * Tq).int()
+    cu[::2] = -5
+    q = torch.ones((Tq, 1, D), dtype=torch.bfloat16, device="cuda")
+    rows = torch.full((Tq + 64, 1, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    need = nvq.nvq_attn_chunk_workspace_bytes(nvq.NVQ_KV_BF16, B, Tq, 1, 1, D, pages, page)
+    room = torch.full((need + (64 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    nvq.nvq_attn_chunk(q, kc, vc, table, cu, lengths, rows[:Tq], workspace=room[:need])
+    torch.cuda.synchronize()
+    assert bool((room[need:] == 0x5A).all()) and bool((rows[Tq:] == 7.0).all())

@@ -60,6 +60,17 @@ def test_powers_that_change_along_the_keys(way):
     go("bf16", [(70, 500), (60, 1500)], 16, 1, 64, 16, 13, width_v=2.0, rows_of=rows, some=25)
 
 
+@pytest.mark.parametrize("more", [1.0, 1e-4])
+def test_smallest_scales(more):
+    """Blocks whose scale is the smallest that there is, 2^-24, or 0; and a sequence of zeros alone."""
+    r = np.random.Generator(np.random.PCG64(4))
+
+    def rows(n, w):
+        return np.clip(r.standard_normal((n, 1, 64)) * w, -3.2 * w, 3.2 * w) * (more if w < 1 else 1.0)
+
+    go("bf16", [(70, 200), (60, 700)], 16, 1, 64, 16, 14, width_v=2.5e-6, rows_of=rows, some=25)
+
+
 @pytest.mark.parametrize("type_", ["f16", "bf16"])
 @pytest.mark.parametrize("window", [0, 70])
 def test_non_finite_rows_reach_only_queries_that_see_them(window, type_):
