@@ -9,12 +9,28 @@
 // walks the keys in tiles of 64 with a running maximum and sum.  Both products are
 // v_mfma_f32_32x32x16 with rows as columns:
 //     S^T [keys][32 rows] = K Q^T,      O^T [D][32 rows] += V^T P^T
-// Few rows behind many keys are split over workgroups by keys and joined in order by a second kernel.
+// Tiles are in LDS twice: while one is multiplied, the next is on its way (16-bit caches: straight from memory, with
+// no register in between; Q8_0: through registers, converted between the score products), one barrier a tile.
+// Probabilities and queries stay in registers.  A tile's keys and values that are not in the cache's last pages are
+// zeros; masks are looked at only in tiles that some row does not see whole.
 //
-// Q8_0.  Codes times scales, rounded to binary16's 11 bits, are the operands, with one power of two a
-// tile taken out of the scales: scores take it back, the accumulator is held in units of the
-// largest value power so far.  A row's channels keep the cache's order (interleaved over its
+// Work split: few rows behind many keys are split over workgroups by keys, in parts whose length is chosen on the
+// device from the lengths, and joined in order by a second kernel (results do not depend on timing).
+//
+// Q8_0.  Codes times scales, rounded to binary16, are the operands, with one power of two a tile taken out of the
+// scales: scores take the keys' back, the accumulator is held in units of the values', which changes where
+// a tile's largest scale leaves it by 2^4 either way.  A row's channels keep the cache's order (interleaved over its
 // blocks), which is as good as any for the contraction: queries and results are permuted instead.
+//
+// Roundings to 16 bits: Q8_0's operands (11 bits; what is behind them has 8), probabilities (to the operands' type, as
+// in the prompt's kernel; the sum that divides them is of the rounded ones), results.
+//
+// What bounds it.  Many queries: the matrix and the vector unit in turn.  2048 queries (40 heads of 128 on 8) behind
+// 14336 keys in bfloat16 take 635 us, 1015 TFLOP/s, where a large matrix product reaches 1117; matrix
+// instructions are issued 47 % of the time, vector ones 37 %, no LDS conflicts.  Over Q8_0 715 us.  Heads of 64 have half
+// the products to the same softmax: 1024 queries, window of 4096, 59 us, 580 TFLOP/s.  Few queries: memory.  32 single
+// tokens behind 8000 keys each, bfloat16, 190 us (5.5 TB/s); a mixed batch of 24, 55 us.  The smallest calls are
+// latency: 16 tokens behind 484 keys 15 us in the two kernels.
 #include "attn_tiles.h"
 #include "nvq_launch.h"
 
@@ -24,15 +40,22 @@ namespace {
 
 constexpr int kWaves = kTileWaves;
 constexpr int kRows = 32 * kWaves;  // of a workgroup
-constexpr int kMinPart = 1;  // tiles: the shortest part
-constexpr int kAhead = 4;    // products that the scores' operands are read ahead
+// The shortest part, in tiles: 16 tokens behind 484 keys take 15 us with parts of one tile, 19 with parts of four
+// (a tile's latency against one more part to join); longer calls the same.
+constexpr int kMinPart = 1;
+constexpr int kAhead = 4;  // products that the scores' operands are read ahead
 // Parts for one round of workgroups over the chip, or for two where a workgroup's share of the call is more than
-// this many tiles (the last round's idle places then cost less).
-constexpr int kOneRound = 32, kRounds = 2;
+// kOneRound tiles, so that what the last one leaves idle weighs less.  40 heads of 128 on 8, bfloat16, one round and two: a
+// prompt of 2048 tokens (40 tiles) 63 and 91 us, 32 tokens behind 8000 keys each (62) 190 and 198; 1024 queries of
+// 16384 keys (160) 389 and 346, 2048 (320) 701 and 638.  Three: 636 and no gain elsewhere.
+constexpr int kOneRound = 128, kRounds = 2;
 // Q8_0 is turned into binary16 first from so many rows (query, head) a sequence on, on average, in so much workspace
-// at most.
+// at most: a tile is then converted once for all row tiles, and read from there in twice the bytes.  One sequence, 5
+// heads to a key head: 100 queries behind 32768 keys 112 us without and 142 with it, 205 behind 16000 122 and 122 (1025
+// rows), 512 of 16384 259 and 226, 2048 929 and 747.
 constexpr int64_t kExpandRows = 8 * kRows, kExpandBytes = int64_t(1) << 30;
-// Workgroups that the chip holds at once (by registers), for nb 32-blocks a row
+// Workgroups that the chip holds at once (by registers), for nb 32-blocks a row: more parts than that wait (1024 queries
+// of heads of 64, planned for 4 to a compute unit: 62 us for 59)
 constexpr int places(int nb) { return 256 * (nb <= 2 ? 3 : nb <= 4 ? 2 : 1); }
 
 struct ChunkArgs {
@@ -560,7 +583,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
         if (kb) turn(ks);
       }
     // Order asked of the compiler: the operands' reads stay kAhead products ahead (left alone, it reads each right before
-    // its product: 650 us for 635 of 2048 queries behind 14336 keys, 2 and 4 ahead alike, 8 slower again)
+    // its product: 650 us for 635 of 2048 bfloat16 queries behind 14336 keys; 2 ahead 635, 8 ahead 641)
     __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);  // LDS reads
 #pragma unroll
     for (int i = 0; i < 4 * NB; ++i) {
@@ -785,7 +808,8 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
 
 // Q8_0 into binary16, tile blockIdx.x of key head and sequence blockIdx.y, where a sequence has so many row tiles
 // that converting each tile once and reading twice the bytes costs less than converting it in every one of
-// them.  A page number outside the cache makes NaN of its keys.
+// them.  Bound by memory: 16384 keys of 8 key heads of 128, 36 MB read and 67 written, 31 us.  A page number outside
+// the cache makes NaN of its keys.
 template <int NB>
 __global__ __launch_bounds__(64 * kWaves) void attn_chunk_expand_kernel(ChunkArgs a) {
   typedef Cached<NVQ_KV_Q8_0, NB> C;
@@ -838,7 +862,8 @@ __global__ __launch_bounds__(64 * kWaves) void attn_chunk_expand_kernel(ChunkArg
   }
 }
 
-// Joins the parts of one row tile of a key head in their order: a workgroup takes 32 channels of its rows.
+// Joins the parts of one row tile of a key head in their order: a workgroup takes 32 channels of its rows, so that a
+// short call's few row tiles are on many compute units.  Latency: about 4 us of a small call.
 template <int FMT, int NB>
 __global__ __launch_bounds__(64 * kWaves) void attn_chunk_join_kernel(ChunkArgs a) {
   typedef Cached<FMT, NB> C;
