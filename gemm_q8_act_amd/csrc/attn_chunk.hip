@@ -54,9 +54,10 @@ constexpr int kOneRound = 128, kRounds = 2;
 // heads to a key head: 100 queries behind 32768 keys 112 us without and 142 with it, 205 behind 16000 122 and 122 (1025
 // rows), 512 of 16384 259 and 226, 2048 929 and 747.
 constexpr int64_t kExpandRows = 8 * kRows, kExpandBytes = int64_t(1) << 30;
-// Workgroups that the chip holds at once (by registers), for nb 32-blocks a row: more parts than that wait (1024 queries
-// of heads of 64, planned for 4 to a compute unit: 62 us for 59)
-constexpr int places(int nb) { return 256 * (nb <= 2 ? 3 : nb <= 4 ? 2 : 1); }
+// Workgroups that a call is planned for at once, for nb 32-blocks a row: about what registers hold to a compute unit.
+// Measured against one more: heads of 64, 1024 queries in a window 59 and 62 us; of 96, 512 queries of 4096 keys 51 and
+// 59; of 32, three, four and five: 32 tokens behind 8000 Q8_0 keys each 75, 68 and 68 us, 8 x 16 of 2000 keys 16, 16 and 19.
+constexpr int places(int nb) { return 256 * (nb <= 1 ? 4 : nb <= 2 ? 3 : nb <= 4 ? 2 : 1); }
 
 struct ChunkArgs {
   const uint16_t* q;
