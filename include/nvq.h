@@ -512,7 +512,7 @@ nvq_status nvq_rope_table(const double* inv_freq, int64_t P, int64_t R, float* t
  * output NULL.  An output may be its own input (same address, strides and type); otherwise it
  * overlaps none of the inputs.  q_weight, k_weight: float32 [D] on the device, NULL: no norm of
  * those heads; eps not negative.  R a multiple of 4, 4 <= R <= D; T * (Hq + Hkv) below 2^31.  Arithmetic
- * and sums in float32, one rounding to out_type. */
+ * and sums in float32 (a head whose squares pass its range becomes 0), one rounding to out_type. */
 enum { NVQ_ROPE_HALVES = 0, NVQ_ROPE_NEIGHBOURS = 1 };
 nvq_status nvq_qk_norm_rope(int type, int out_type, const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
                             int64_t k_stride_t, int64_t k_stride_h, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
@@ -603,9 +603,9 @@ nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v
  * there).  Pages whose keys no query sees (before the windows, behind the end) are not looked up.
  * Scores, softmax statistics and accumulation are float32; the probabilities enter the second product rounded
  * once to 16 bits (binary16 over Q8_0: 11 bits down to 2^-25 of the largest, as in nvq_attn_prompt).  Over
- * Q8_0 the operands are code * scale rounded to binary16's 11 bits: of keys down to 2^-36 of the largest in
- * their 64-key tile, of values down to 2^-36 of the largest that the query's tiles have had so far; bfloat16
- * queries' channels are held to 2^-32 of the largest.  Keys and values that a query does not see never
+ * Q8_0 the operands are code * scale rounded to binary16 in a unit of their 64-key tile: 11 bits for blocks whose
+ * scale is at least 2^-18 (keys) or 2^-15 (values) of the tile's largest, fewer below, none below 2^-28 and 2^-25;
+ * bfloat16 queries' channels are held to 2^-32 of the largest.  Keys and values that a query does not see never
  * matter, whatever they hold.  An infinity or NaN in a value row shows, as one of them, in its channel (over
  * Q8_0 in its 32-channel block) of the queries that see it, in a key row in all of theirs.  out overlaps none of
  * the inputs.
