@@ -11,7 +11,7 @@
 //     S^T [keys][32 rows] = K Q^T,      O^T [D][32 rows] += V^T P^T
 // Tiles are in LDS twice: while one is multiplied, the next is on its way (16-bit caches: straight from memory, with
 // no register in between; Q8_0: through registers, converted between the score products), one barrier a tile.
-// Probabilities and queries stay in registers.  A tile's keys and values that are not in the cache's last pages are
+// Probabilities and queries stay in registers.  Rows of a tile that no row of the work sees are not read and come as
 // zeros; masks are looked at only in tiles that some row does not see whole.
 //
 // Work split: few rows behind many keys are split over workgroups by keys, in parts whose length is chosen on the

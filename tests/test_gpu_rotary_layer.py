@@ -165,3 +165,33 @@ def test_captured_serving_step(cache):
         assert ((x - z).abs() <= (2.0 ** -8 + score) * largest + 2.0 ** -8 * (x.abs() + z.abs())).all()
     for x, z in zip([*eager[0], *[s for s in eager[1] if s is not None]], [*replayed[0], *[s for s in replayed[1] if s is not None]]):
         assert torch.equal(x, z)
+
+
+@pytest.mark.parametrize("fmt", ["q8_0", "bf16"])
+def test_pages_past_32_bit_offsets(fmt):
+    """The same tokens written to, and read from, the last pages of a cache of more than 4 GiB a tensor and a small one."""
+    torch = torch_dev()
+    Hq, Hkv, D, page, n = 10, 2, 128, 256, 700
+    pages = -(-n // page)
+    g = torch.Generator("cuda").manual_seed(9)
+    y = torch.randn((n, Hq + 2 * Hkv, D), generator=g, device="cuda")
+    turns = torch.from_numpy(nvq.nvq_rope_table(n, D)).cuda()
+    at = torch.arange(n, device="cuda")
+    results = []
+    for n_pages in (pages, (1 << 32) // (Hkv * page * D * (1 if fmt == "q8_0" else 2)) + pages + 5):
+        say(f"pages past 32 bits: {fmt} {n_pages}")
+        dtype = torch.int8 if fmt == "q8_0" else torch.bfloat16
+        codes = [torch.empty((n_pages, Hkv, page, D), dtype=dtype, device="cuda") for _ in "kv"]
+        scales = [torch.empty((n_pages, Hkv, page, D // 32), dtype=torch.float16, device="cuda") if fmt == "q8_0" else None for _ in "kv"]
+        table = (n_pages - 1 - torch.arange(pages, device="cuda"))[None].int()
+        q = torch.empty((n, Hq, D), dtype=torch.bfloat16, device="cuda")
+        nvq.nvq_rope_kv_write(y[:, :Hq], y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:], turns, at.int(), table[0].long()[at // page] * page + at % page, q, *codes,
+                              *scales)
+        lengths = torch.tensor([n], dtype=torch.int32, device="cuda")
+        a, b = torch.empty_like(q), torch.empty_like(q[-1:])
+        nvq.nvq_attn_chunk(q, *codes, table, torch.tensor([0, n], dtype=torch.int32, device="cuda"), lengths, a, *scales, window=400, sinks=3)
+        nvq.nvq_attn_decode_window(q[-1:], *codes, table, lengths, b, *scales, window=400, sinks=3)
+        results.append([host(x.float()) for x in (q, a, b)])
+        del codes, scales
+    for x, z in zip(*results):
+        assert np.isfinite(x).all() and (x == z).all()
