@@ -53,7 +53,9 @@ __device__ __forceinline__ void store_halves(void* p, const uint16_t (&v)[N]) {
       reinterpret_cast<u32x4*>(p)[i] = w;
     }
   } else if constexpr (N % 4 == 0) {
-    *reinterpret_cast<u32x2*>(p) = u32x2{v[0] | ((uint32_t)v[1] << 16), v[2] | ((uint32_t)v[3] << 16)};
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      reinterpret_cast<u32x2*>(p)[i] = u32x2{v[4 * i] | ((uint32_t)v[4 * i + 1] << 16), v[4 * i + 2] | ((uint32_t)v[4 * i + 3] << 16)};
   } else if constexpr (N % 2 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) reinterpret_cast<uint32_t*>(p)[i] = v[2 * i] | ((uint32_t)v[2 * i + 1] << 16);
@@ -72,8 +74,11 @@ __device__ __forceinline__ void load_halves(const void* p, uint16_t (&v)[N]) {
       for (int j = 0; j < 4; ++j) v[8 * i + 2 * j] = (uint16_t)w[j], v[8 * i + 2 * j + 1] = (uint16_t)(w[j] >> 16);
     }
   } else if constexpr (N % 4 == 0) {
-    const u32x2 w = *reinterpret_cast<const u32x2*>(p);
-    v[0] = (uint16_t)w[0], v[1] = (uint16_t)(w[0] >> 16), v[2] = (uint16_t)w[1], v[3] = (uint16_t)(w[1] >> 16);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const u32x2 w = reinterpret_cast<const u32x2*>(p)[i];
+      v[4 * i] = (uint16_t)w[0], v[4 * i + 1] = (uint16_t)(w[0] >> 16), v[4 * i + 2] = (uint16_t)w[1], v[4 * i + 3] = (uint16_t)(w[1] >> 16);
+    }
   } else if constexpr (N % 2 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
