@@ -226,12 +226,26 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(Args a) {
       for (int b = 0; b < NB; ++b) to_floats<T, E>(raw_y[b], y[b]);
     }
     if (weight) {
-      float s = 0.0f;
+      const auto mean_square = [&](float eps) __attribute__((always_inline)) {
+        float s = 0.0f;
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < E; ++i) s = __builtin_fmaf(x[b][i], x[b][i], s);
-      const float norm = __builtin_amdgcn_rsqf(lanes_sum<LANES>(s) * (1.0f / (32 * NB)) + r.eps);
+          for (int i = 0; i < E; ++i) s = __builtin_fmaf(x[b][i], x[b][i], s);
+        return lanes_sum<LANES>(s) * (1.0f / (32 * NB)) + eps;
+      };
+      float mean = mean_square(r.eps);
+      if (mean < 0x1p-100f) {  // squares that float32 may not hold (a row's lanes agree): elements, below 2^-46, times 2^100, eps by its square
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            x[b][i] *= 0x1p100f;
+            if constexpr (PAIR == kApart) y[b][i] *= 0x1p100f;
+          }
+        mean = mean_square(r.eps * 0x1p100f * 0x1p100f);
+      }
+      const float norm = __builtin_amdgcn_rsqf(mean);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
