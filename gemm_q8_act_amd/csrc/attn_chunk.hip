@@ -90,6 +90,18 @@ __device__ __forceinline__ int tiles_seen(const ChunkArgs& a, int n) {
   return min(all, (min(a.sinks, n) + kKeys - 1) / kKeys + (a.window + kRows - 1 + kKeys - 1) / kKeys + 1);
 }
 
+// Scores (base 2) from whose maximum so large on a difference may round to 1 and more: a probability would pass the range that
+// Range leaves it, and with larger ones every range, either way.  There differences come first, of scores rounded as the
+// maximum was, and end where it may be passed.
+constexpr float kFar = 0x1p22f;
+__device__ __forceinline__ float m_finite(float m) { return m == -__builtin_inff() ? 0.0f : m; }
+
+__device__ __forceinline__ float difference(float s, float factor, float m) {
+#pragma clang fp contract(off)
+  const float score = s * factor;
+  return score - m;
+}
+
 // A value that all lanes share, in a scalar register (what a division leaves in a vector one would drag all that
 // follows along)
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -466,6 +478,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
 #pragma unroll
     for (int j = 0; j < 16; ++j) acc[d][j] = 0.0f;
   float m = -__builtin_inff(), l = 0.0f;
+  bool far = false;  // some row's maximum passes kFar
   int unit = kNone;  // Q8_0: the accumulator is in units of 2^unit
 
   // What is not finite in a value row must not meet a probability of 0 in rows that do not see it: it stays out of
@@ -612,8 +625,19 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
 #pragma unroll
       for (int d = 0; d < NB; ++d) acc[d] *= f;
       m = m_new;
+      far = __any(fabsf(m_finite(m)) >= kFar);
     }
-    const float base = score_base<T>(m);
+    float base = score_base<T>(m), times = factor;
+    if (far) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float x = difference(s[kb][j], factor, m_finite(m));
+          s[kb][j] = x > Range<T>::SLACK ? Range<T>::SLACK : x;
+        }
+      base = -Range<T>::SHIFT, times = 1.0f;
+    }
     Frag pf[2][2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
@@ -621,8 +645,8 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float x = exp2_fast(__builtin_fmaf(s[kb][8 * h + 2 * j], factor, -base));
-          const float y = exp2_fast(__builtin_fmaf(s[kb][8 * h + 2 * j + 1], factor, -base));
+          const float x = exp2_fast(__builtin_fmaf(s[kb][8 * h + 2 * j], times, -base));
+          const float y = exp2_fast(__builtin_fmaf(s[kb][8 * h + 2 * j + 1], times, -base));
           pf[kb][h].v[j] = pack_pair<T>(x, y);
           l = add_pair<T>(pf[kb][h].v[j], l);
         }
