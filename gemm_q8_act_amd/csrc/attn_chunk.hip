@@ -19,7 +19,11 @@
 //
 // Q8_0.  Codes times scales, rounded to binary16, are the operands, with one power of two a tile taken out of the
 // scales: scores take the keys' back, the accumulator is held in units of the values', which changes where
-// a tile's largest scale leaves it by 2^4 either way.  A row's channels keep the cache's order (interleaved over its
+// a tile's largest scale leaves it by 2^4 either way.  Scales far below the tile's largest lose bits by it, as it may be where
+// every row sees both; a tile of which some row does not see all has no part in the loop if a scale does, and is computed in float32
+// behind it, key by key (about 2 us a key for heads of 128: 16 queries whose last key's values are 2^24 times the others' 113 us
+// for 17).  What that costs calls without such tiles: 16 tokens behind 484 keys 16.4 us for 15.7, 2048 queries behind 14336 keys 1 %, a
+// batch that is not turned first up to 6 %.  A row's channels keep the cache's order (interleaved over its
 // blocks), which is as good as any for the contraction: queries and results are permuted instead.
 //
 // Roundings to 16 bits: Q8_0's operands (11 bits; what is behind them has 8), probabilities (to the operands' type, as
@@ -59,6 +63,8 @@ constexpr int64_t kExpandRows = 8 * kRows, kExpandBytes = int64_t(1) << 30;
 // 59; of 32, three, four and five: 32 tokens behind 8000 Q8_0 keys each 75, 68 and 68 us, 8 x 16 of 2000 keys 16, 16 and 19.
 constexpr int places(int nb) { return 256 * (nb <= 1 ? 4 : nb <= 2 ? 3 : nb <= 4 ? 2 : 1); }
 
+constexpr int kWide = 0x100;  // in units
+
 struct ChunkArgs {
   const uint16_t* q;
   uint16_t* out;
@@ -77,9 +83,9 @@ struct ChunkArgs {
   int slot_waves;  // wavefronts' rows that a part's slot holds
   int slots;       // that there are
   // Q8_0 turned into binary16 before (kExpanded): rows [sequence][key head][tile][64] in the cache's channel order, and of
-  // each tile the powers of two that its keys (lower half) and values were divided by
+  // each tile the powers of two that its keys (lowest byte) and values (upper half) were divided by
   uint16_t *keys, *values;
-  int* units;
+  int* units;      // (kWide besides where scales lost bits by it)
   int tiles;       // of a sequence there
 };
 
@@ -210,6 +216,10 @@ __device__ __forceinline__ Rows rows_of(const ChunkArgs& a, const Work& w) {
   return r;
 }
 
+// Tiles of a row tile that some row sees and some row does not see whole, at most: 128 rows' places lie within 128 keys, so
+// up to 3 tiles hold the ends of what they see and 3 the beginnings of their windows, and one the last of the first keys
+constexpr int kPartly = 8;
+
 constexpr int kExpanded = 16;
 template <int FMT, int NB>
 struct Cached {
@@ -294,6 +304,9 @@ constexpr int kNone = -1000;
 __device__ __forceinline__ int exponent_of(uint32_t bits) {
   return bits >= 0x400u ? (int)(bits >> 10) - 14 : bits ? 8 - __builtin_clz(bits) : kNone;
 }
+// The power of two that takes a scale of exponent e to the highest place where its largest code is a binary16 number, which leaves
+// the most below it (and not past what scale_down has: a scale so small is exact there)
+__device__ __forceinline__ int highest(int e) { return max(e - 9, -30); }
 // Scales times 2^-e, in two steps that binary16 holds
 template <int N>
 __device__ __forceinline__ typename Dwords<N>::type scale_down(typename Dwords<N>::type d, int e) {
@@ -305,6 +318,16 @@ __device__ __forceinline__ typename Dwords<N>::type scale_down(typename Dwords<N
     d[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, x) * f * g);
   }
   return d;
+}
+
+// Whether scales x lost bits in it: some came out below the normal range (what was subnormal before is exact where it does not)
+template <int N>
+__device__ __forceinline__ bool lost_bits(typename Dwords<N>::type x, typename Dwords<N>::type scaled) {
+  uint32_t lost = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    lost |= (uint32_t)(((scaled[i] & 0x7C00u) == 0) & ((x[i] & 0x7FFFu) != 0)) | (uint32_t)(((scaled[i] & 0x7C000000u) == 0) & ((x[i] & 0x7FFF0000u) != 0));
+  return lost != 0;
 }
 
 // The scales of row `row_in` of a group
@@ -346,6 +369,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
   __shared__ __align__(16) uint8_t s_keys[2 * S::BYTES], s_values[2 * S::BYTES];
   __shared__ __align__(16) uint32_t s_top[4][kWaves];  // Q8_0: the groups' largest scales, keys' in the upper half
   __shared__ int s_bad, s_broken;  // a page number outside the cache; a value that is not finite in a tile of which some row does not see all
+  __shared__ int s_wide[kPartly];  // Q8_0: the part's partly seen tiles, in order: not 0 if left out at first
   const int tid = (int)threadIdx.x, lane = tid & 63, c = lane & 31, hi = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int item = uniform((int)blockIdx.x / a.Hkv), kvh = (int)blockIdx.x - item * a.Hkv;
@@ -356,6 +380,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
   const bool split = rt.tiles > w.part_tiles;
   if (w.part > 0 && t_begin >= rt.tiles) return;
   if (tid == 0) s_bad = s_broken = 0;
+  if (C::Q8 && tid < kPartly) s_wide[tid] = 0;
 
   // A lane's row; past the last row it again, which is not stored
   const bool mine = 32 * wave < rt.count;
@@ -369,7 +394,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
   };
   const int place = row_of(c).place;
   const int place_first = __builtin_amdgcn_readlane(place, 0), place_last = __builtin_amdgcn_readlane(place, 31);
-  const auto seen = [&](int key) __attribute__((always_inline)) { return (key <= place) & ((key > place - a.window) | (key < a.sinks)); };
+  const auto seen_by = [&](int place, int key) __attribute__((always_inline)) { return (key <= place) & ((key > place - a.window) | (key < a.sinks)); };
 
   // Its query, 16 places of the cache's channel order at a time, on the way before the keys' place is known
   Frag qf[2 * NB];
@@ -417,7 +442,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
   };
   const auto partly = [&](int t) __attribute__((always_inline)) {  // some row does not see some key of the tile
     const int key0 = tile_key(t);
-    return key0 + kKeys - 1 > rt.first || (key0 <= rt.last - a.window && key0 + kKeys - 1 >= a.sinks);
+    return (key0 + kKeys - 1 > rt.first) | ((key0 <= rt.last - a.window) & (key0 + kKeys - 1 >= a.sinks));
   };
 
   // 16-bit caches: straight into LDS, 64 pieces of 16 bytes a load, in LDS order.  Rows that are not read come
@@ -464,6 +489,16 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
     const u32x4 x = *reinterpret_cast<const u32x4*>(s_top[slot]);
     return (uint32_t)__builtin_amdgcn_readfirstlane((int)max_halves(max_halves(x[0], x[1]), max_halves(x[2], x[3])));
   };
+  // Rows between the first keys and the windows, in a group that is read: their scales become 0, so that they have no
+  // part in the tile's largest
+  const auto hide = [&](int t, Scales& k, Scales& v) __attribute__((always_inline)) {
+    if (tile_key(t) < rt.start) {
+      const int key = tile_key(t) + 16 * wave + row_in;
+      const bool unseen = (key >= rt.sink) & (key < rt.start);
+#pragma unroll
+      for (int i = 0; i < C::SCALES; ++i) k[i] = unseen ? 0u : k[i], v[i] = unseen ? 0u : v[i];
+    }
+  };
   // Piece i of the lane's part of a row, with the scales times 2^-e, into a tile
   const auto convert = [&](uint8_t* tile, Codes codes, Scales scales, int i, bool keys) __attribute__((always_inline)) {
     if constexpr (C::Q8) {
@@ -483,19 +518,31 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
 
   // What is not finite in a value row must not meet a probability of 0 in rows that do not see it: it stays out of
   // a tile that has keys that some row does not see, and rows that see it get it behind the last one.
-  const auto keep_finite = [&](int t, Scales d) __attribute__((always_inline)) {
-    if (partly(t)) {
-      uint32_t found = 0;
+  const auto keep_finite = [&](Scales d) __attribute__((always_inline)) {
+    uint32_t found = 0;
 #pragma unroll
-      for (int i = 0; i < C::SCALES; ++i) found |= not_finite<_Float16>(d[i]);
-      if (__any(found != 0)) {
-        s_broken = 1;
+    for (int i = 0; i < C::SCALES; ++i) found |= not_finite<_Float16>(d[i]);
+    if (__any(found != 0)) {
+      s_broken = 1;
 #pragma unroll
-        for (int i = 0; i < C::SCALES; ++i) d[i] &= ~not_finite<_Float16>(d[i]);
-      }
+      for (int i = 0; i < C::SCALES; ++i) d[i] &= ~not_finite<_Float16>(d[i]);
     }
     return d;
   };
+  // Q8_0: a tile's scales times their powers of two.  Of a partly seen tile none may lose bits by it, to a row that others
+  // see: the tile, the part's number `number` of them, is left out at first
+  const auto scale_both = [&](bool part_seen, int number, Scales& k, int ek, Scales& v, int ev) __attribute__((always_inline)) {
+    const Scales k_old = k;
+    if (part_seen) v = keep_finite(v);
+    const Scales v_old = v;
+    k = scale_down<C::SCALES>(k_old, ek), v = scale_down<C::SCALES>(v_old, ev);
+    if (part_seen) {
+      if (__any(lost_bits<C::SCALES>(k_old, k) | lost_bits<C::SCALES>(v_old, v))) s_wide[number] = 1;
+    }
+  };
+  int at = 0;                         // partly seen tiles so far
+  bool here = partly(t_begin);        // this tile is one
+  bool any_wide = false;              // one was left out
   // the same for a 16-bit tile that is in LDS: a wavefront its group's rows
   const auto check_values = [&](int slot) __attribute__((always_inline)) {
     uint8_t* p = s_values + slot * S::BYTES + wave * 16 * S::ROW + 16 * lane;
@@ -581,8 +628,8 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
       value_offset[d] = in_vgpr((uint32_t)(in * S::ROW + 16 * S::value_piece(in, 4 * d + 2 * half + ((jj & 3) >> 1)) + 8 * (jj & 1)));
   }
 
-  // Tile t in a slot, seen with scores times `factor`; between the first products, `turn` has its turns
-  const auto step = [&](int t, int slot, float factor, auto turn) __attribute__((always_inline)) {
+  // Tile t in a slot, seen with scores times `factor`, or (wide) not at all; between the first products, `turn` has its turns
+  const auto step = [&](int t, int slot, float factor, bool wide, auto turn) __attribute__((always_inline)) {
     floatx16 s[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
@@ -605,12 +652,13 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
       if (i + kAhead < 4 * NB) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
     const int key0 = tile_key(t);
-    if (key0 + kKeys - 1 > place_first || (key0 <= place_last - a.window && key0 + kKeys - 1 >= a.sinks)) {
+    if (wide || key0 + kKeys - 1 > place_first || (key0 <= place_last - a.window && key0 + kKeys - 1 >= a.sinks)) {
+      const int from = wide ? -1 : place;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          if (!seen(key0 + 32 * kb + 8 * (j >> 2) + 4 * hi + (j & 3))) s[kb][j] = -__builtin_inff();
+          if (!seen_by(from, key0 + 32 * kb + 8 * (j >> 2) + 4 * hi + (j & 3))) s[kb][j] = -__builtin_inff();
     }
     float top = s[0][0];
 #pragma unroll
@@ -669,11 +717,12 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
   // accumulator's unit from that tile on
   const auto key_unit = [&](uint32_t x) __attribute__((always_inline)) {
     const int e = exponent_of(x >> 16);
-    return e == kNone ? 0 : e - 5;
+    return e == kNone ? 0 : highest(e);
   };
-  const auto value_unit = [&](uint32_t x) __attribute__((always_inline)) {
+  const auto value_unit = [&](bool part_seen, uint32_t x) __attribute__((always_inline)) {
     const int e = exponent_of(x & 0xFFFFu);
-    return e == kNone || (unit != kNone && e - unit <= 9 && e - unit >= 2) ? unit : e - 5;
+    const int u = part_seen ? highest(e) : unit != kNone && e - unit <= 9 && e - unit >= 2 ? unit : e - 5;
+    return e == kNone ? unit : u;
   };
   // base 2, of a score with the keys in units of 2^e (not 0, which would make NaN of a masked score)
   const auto factor_of = [&](int e) __attribute__((always_inline)) { return fmaxf(__builtin_amdgcn_ldexpf(to_log2, e), 1e-37f); };
@@ -695,13 +744,15 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
   if (t_begin < t_end) {
     float factor = 0.0f;
     if constexpr (C::Q8) {
+      hide(t_begin, k0_d, v0_d);
+      hide(t_begin + 1, k_scales, v_scales);
       publish(2, k0_d, v0_d);
       publish(1, k_scales, v_scales);
       barrier();
       const uint32_t x = published(2);
       const int e = key_unit(x);
-      unit = value_unit(x);
-      k0_d = scale_down<C::SCALES>(k0_d, e), v0_d = scale_down<C::SCALES>(keep_finite(t_begin, v0_d), unit == kNone ? 0 : unit);
+      unit = value_unit(here, x);
+      scale_both(here, 0, k0_d, e, v0_d, unit == kNone ? 0 : unit);
 #pragma unroll
       for (int i = 0; i < NB; ++i) convert(s_keys, k0, k0_d, i, true);
 #pragma unroll
@@ -719,10 +770,12 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
       uint8_t* const keys = s_keys + (slot ^ 1) * S::BYTES;
       uint8_t* const values = s_values + (slot ^ 1) * S::BYTES;
       if constexpr (C::Q8) {
-        const Scales k_next = load_scales(a.c.k_d, g2), v_next = load_scales(a.c.v_d, g2);
+        Scales k_next = load_scales(a.c.k_d, g2), v_next = load_scales(a.c.v_d, g2);
+        const bool wide = here && uniform(s_wide[at]) != 0;
+        at += here, any_wide |= wide, here = partly(t + 1);
         const uint32_t x = published(slot ^ 1);
-        const int e = key_unit(x), u = value_unit(x);
-        k_scales = scale_down<C::SCALES>(k_scales, e), v_scales = scale_down<C::SCALES>(keep_finite(t + 1, v_scales), u == kNone ? 0 : u);
+        const int e = key_unit(x), u = value_unit(here, x);
+        scale_both(here, at, k_scales, e, v_scales, u == kNone ? 0 : u);
         const auto turn = [&](int j) __attribute__((always_inline)) {
           if (j < NB)
             convert(keys, k_codes, k_scales, j, true);
@@ -730,7 +783,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
             convert(values, v_codes, v_scales, j - NB, false);
         };
         if (mine) {
-          step(t, slot, factor, turn);
+          step(t, slot, factor, wide, turn);
         } else {
 #pragma unroll
           for (int j = 0; j < 2 * NB; ++j) turn(j);
@@ -738,6 +791,7 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
         use_unit(u);
         factor = factor_of(e);
         k_codes = load_codes(a.c.k, g2), v_codes = load_codes(a.c.v, g2);
+        hide(t + 2, k_next, v_next);
         publish(slot, k_next, v_next);
         k_scales = k_next, v_scales = v_next;
       } else {
@@ -753,13 +807,16 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
             buffer_to_lds(vb, value_from[j - NB], (uint32_t)uniform((int)(values_at + (slot ^ 1) * S::BYTES + 1024 * (j - NB))));
         };
         float f = a.scale_log2;
+        bool wide = false;
         if constexpr (C::EXPANDED) {
-          f = factor_of((int16_t)next_unit);
+          f = factor_of((int8_t)next_unit);
+          wide = (next_unit & kWide) && partly(t);
+          any_wide |= wide;
           use_unit(next_unit >> 16);
           next_unit = unit_of(t + 1);
         }
         if (mine) {
-          step(t, slot, f, turn);
+          step(t, slot, f, wide, turn);
         } else {
 #pragma unroll
           for (int j = 0; j < 2 * NB; ++j) turn(j);
@@ -776,58 +833,146 @@ __global__ __launch_bounds__(64 * kWaves, NB <= 4 ? 2 : 1) void attn_chunk_kerne
   if (!mine) return;
   l = sum_32(l);
   const Row row = row_of(in_vgpr((uint32_t)lane) & 31);
+  // From here on arguments are read again, from an address that the compiler does not know: it would keep them all along, and the
+  // loop's scalars go to lanes of vector registers (with 28 of them no operand of the value products was read ahead: 2048 queries
+  // behind 14336 Q8_0 keys 798 us for 724)
+  auto* late = (const __attribute__((address_space(4))) ChunkArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(late));
+  const auto* pages = (const __attribute__((address_space(4))) int32_t*)(late->table + (int64_t)w.b * late->table_stride);
+  if (C::MIXED && unit != kNone) {
+    const float f = __builtin_amdgcn_ldexpf(1.0f, unit);
+#pragma unroll
+    for (int d = 0; d < NB; ++d) acc[d] *= f;
+  }
+  // Tiles that were left out, with codes and scales out of the cache, in float32: lanes have rows as before, and half of their channels.
+  // Rare, so it is kept from costing the loop registers: the accumulator waits where the tiles were.
+  if constexpr (C::MIXED) {
+    if (any_wide) {
+      floatx4* const mem = reinterpret_cast<floatx4*>((wave & 2 ? s_values : s_keys) + (wave & 1) * S::BYTES) + lane;
+#pragma unroll
+      for (int d = 0; d < NB; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mem[(4 * d + i) * 64] = floatx4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+      // words 2 x + hi of a row are the lane's, of keys and values alike: pairs 4 x + 2 hi and + 1 in the cache's order
+      uint32_t q[8 * NB];
+      {
+        const uint16_t* query = late->q + (int64_t)(w.s.q0 + row.query) * late->q_t + (int64_t)row.head * late->q_h;
+#pragma unroll
+        for (int x = 0; x < 8 * NB; ++x) q[x] = *reinterpret_cast<const uint32_t*>(query + channel_of<true, NB>(4 * (2 * (x >> 1) + hi) + 2 * (x & 1)));
+      }
+      const float signed_scale = late->flip ? -late->scale_log2 : late->scale_log2;
+      for (int t = t_begin, number = 0; t < t_end; ++t) {
+        if (!partly(t)) continue;
+        const bool left_out = C::Q8 ? uniform(s_wide[number]) != 0 : (unit_of(t) & kWide) != 0;
+        ++number;
+        if (!left_out) continue;
+        const int key_end = min(tile_key(t) + kKeys, rt.end);
+#pragma unroll 1
+        for (int key = tile_key(t); key < key_end; ++key) {
+          const bool visible = (key <= row.place) & ((key > row.place - late->window) | (key < late->sinks));
+          if (!__any(visible)) continue;
+          const int page = pages[key >> late->c.page_shift];
+          const bool out = (uint32_t)page >= (uint32_t)late->c.n_pages;
+          const int64_t from = (((int64_t)(out ? 0 : page) * late->Hkv + kvh) << late->c.page_shift) + (key & ((1 << late->c.page_shift) - 1));
+          uint32_t codes[2][4 * NB];
+          float scales[2][NB];  // of pairs x, x + NB, .. of the lane's
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const uint32_t* words = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(v ? late->c.v : late->c.k) + from * (32 * NB)) + hi;
+            const uint16_t* d = reinterpret_cast<const uint16_t*>(v ? late->c.v_d : late->c.k_d) + from * NB;
+#pragma unroll
+            for (int x = 0; x < 4 * NB; ++x) codes[v][x] = words[2 * x];
+#pragma unroll
+            for (int x = 0; x < NB; ++x) scales[v][x] = f16_bits_to_f32(d[(x + 2 * hi) % NB]);
+          }
+#pragma unroll
+          for (int x = 0; x < NB; ++x) scales[1][x] = visible ? scales[1][x] : 0.0f;
+          const auto element = [&](int v, int x, int y) __attribute__((always_inline)) {  // element y of the lane's word x
+            return scales[v][(4 * x + (y >> 1)) % NB] * (float)(int)(int8_t)(codes[v][x] >> (8 * y));
+          };
+          float s = 0.0f;
+#pragma unroll
+          for (int x = 0; x < 8 * NB; ++x) {
+            float two[2];
+            if (late->type == NVQ_TYPE_F16)
+              unpack_pair<_Float16>(q[x], two);
+            else
+              unpack_pair<__bf16>(q[x], two);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) s = __builtin_fmaf(element(0, x >> 1, 2 * (x & 1) + y), two[y] * signed_scale, s);
+          }
+          s = out ? __builtin_nanf("") : sum_32(s);
+          if (!visible) s = -__builtin_inff();
+          const float m_new = s > m + Range<T>::SLACK ? s : m, f = m_new == m ? 1.0f : exp2_fast(m - m_new);
+          m = m_new;
+          const float p = exp2_fast(s - m_finite(m) + Range<T>::SHIFT);
+          l = l * f + p;
+#pragma unroll
+          for (int i = 0; i < 4 * NB; ++i) {
+            floatx4 x = mem[i * 64] * f;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) x[y] = __builtin_fmaf(p, element(1, i, y), x[y]);
+            mem[i * 64] = x;
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < NB; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const floatx4 x = mem[(4 * d + i) * 64];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[d][4 * i + j] = x[j];
+        }
+    }
+  }
   if (s_broken) {
     for (int t = t_begin; t < t_end; ++t)
       for (int j = partly(t) ? 0 : kKeys; j < kKeys; ++j) {
         const int key = tile_key(t) + j;
-        if (!(key <= row.place && (key > row.place - a.window || key < a.sinks))) continue;
-        const int page = C::EXPANDED ? 0 : table[key >> a.c.page_shift];
-        if ((uint32_t)page >= (uint32_t)a.c.n_pages) continue;
-        const int64_t from = C::EXPANDED ? first_tile * kKeys + key : (((int64_t)page * a.Hkv + kvh) << a.c.page_shift) + (key & page_mask);
+        if (!(key <= row.place && (key > row.place - late->window || key < late->sinks))) continue;
+        const int page = C::EXPANDED ? 0 : pages[key >> late->c.page_shift];
+        if ((uint32_t)page >= (uint32_t)late->c.n_pages) continue;
+        const int64_t from = C::EXPANDED ? first_tile * kKeys + key : (((int64_t)page * late->Hkv + kvh) << late->c.page_shift) + (key & ((1 << late->c.page_shift) - 1));
 #pragma unroll
         for (int d = 0; d < NB; ++d)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int at = 32 * d + 8 * (i >> 2) + 4 * hi + (i & 3);
             if constexpr (C::Q8) {
-              const uint16_t x = reinterpret_cast<const uint16_t*>(a.c.v_d)[from * NB + (at >> 1) % NB];
+              const uint16_t x = reinterpret_cast<const uint16_t*>(late->c.v_d)[from * NB + (at >> 1) % NB];
               if ((x & 0x7C00u) == 0x7C00u) acc[d][i] = __builtin_nanf("");
             } else {
-              const uint16_t x = reinterpret_cast<const uint16_t*>(all_values)[from * (32 * NB) + at];
+              const uint16_t x = reinterpret_cast<const uint16_t*>(C::EXPANDED ? late->values : late->c.v)[from * (32 * NB) + at];
               if (not_finite<T>(x) & 0xFFFFu) acc[d][i] += (float)__builtin_bit_cast(T, x);
             }
           }
       }
   }
   if (s_bad || w.s.bad) l = __builtin_nanf("");
-  if (C::MIXED && unit != kNone) {
-    const float f = __builtin_amdgcn_ldexpf(1.0f, unit);
-#pragma unroll
-    for (int d = 0; d < NB; ++d) acc[d] *= f;
-  }
   if (split) {
-    const int64_t slot = (int64_t)w.slot * a.Hkv + kvh;
-    floatx4* dst = reinterpret_cast<floatx4*>(a.acc) + (slot * a.slot_waves + wave) * (NB * 4 * 64) + lane;
+    const int64_t slot = (int64_t)w.slot * late->Hkv + kvh;
+    floatx4* dst = reinterpret_cast<floatx4*>(late->acc) + (slot * late->slot_waves + wave) * (NB * 4 * 64) + lane;
 #pragma unroll
     for (int d = 0; d < NB; ++d)
 #pragma unroll
       for (int j = 0; j < 4; ++j) dst[(4 * d + j) * 64] = floatx4{acc[d][4 * j], acc[d][4 * j + 1], acc[d][4 * j + 2], acc[d][4 * j + 3]};
     if (hi == 0) {
-      a.stat[slot * (2 * kRows) + 32 * wave + c] = m;
-      a.stat[slot * (2 * kRows) + kRows + 32 * wave + c] = l;
+      late->stat[slot * (2 * kRows) + 32 * wave + c] = m;
+      late->stat[slot * (2 * kRows) + kRows + 32 * wave + c] = l;
     }
     return;
   }
   if (!row.live) return;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a query that sees no key gives zeros
-  uint16_t* out = a.out + (int64_t)(w.s.q0 + row.query) * a.o_t + (int64_t)row.head * a.o_h;
+  uint16_t* out = late->out + (int64_t)(w.s.q0 + row.query) * late->o_t + (int64_t)row.head * late->o_h;
 #pragma unroll
   for (int d = 0; d < NB; ++d)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = acc[d][2 * j] * inv, y = acc[d][2 * j + 1] * inv;
       const int at = channel_of<C::MIXED, NB>(32 * d + 8 * (j >> 1) + 4 * hi + 2 * (j & 1));
-      *reinterpret_cast<uint32_t*>(out + at) = a.type == NVQ_TYPE_F16 ? pack_pair<_Float16>(x, y) : pack_pair<__bf16>(x, y);
+      *reinterpret_cast<uint32_t*>(out + at) = late->type == NVQ_TYPE_F16 ? pack_pair<_Float16>(x, y) : pack_pair<__bf16>(x, y);
     }
 }
 
@@ -839,6 +984,7 @@ template <int NB>
 __global__ __launch_bounds__(64 * kWaves) void attn_chunk_expand_kernel(ChunkArgs a) {
   typedef Cached<NVQ_KV_Q8_0, NB> C;
   __shared__ uint32_t s_top[kWaves];
+  __shared__ int s_lost;
   const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int b = uniform((int)blockIdx.y / a.Hkv), kvh = (int)blockIdx.y - b * a.Hkv;
   const Seq s = load_seq(a, b);
@@ -865,19 +1011,24 @@ __global__ __launch_bounds__(64 * kWaves) void attn_chunk_expand_kernel(ChunkArg
     codes[x] = load_dwords<C::WORDS>(buffer(x ? a.c.v : a.c.k, C::ROW), row_in * C::ROW + seg * (C::ROW / 4));
     d[x] = load_row_scales<NB>(buffer(x ? a.c.v_d : a.c.k_d, 2 * NB), row_in);
   }
+  if (!wanted(key0 + row_in, 1)) {  // between the first keys and the first query's window: no part in the tile's largest
+#pragma unroll
+    for (int i = 0; i < C::SCALES; ++i) d[0][i] = d[1][i] = 0;
+  }
   const uint32_t mine = wave_largest(largest_scale<C::SCALES>(d[0]), largest_scale<C::SCALES>(d[1]));
   if (lane == 0) s_top[wave] = mine;
+  if (threadIdx.x == 0) s_lost = 0;
   __syncthreads();
   const uint32_t top = (uint32_t)uniform((int)max_halves(max_halves(s_top[0], s_top[1]), max_halves(s_top[2], s_top[3])));
-  // the largest scale of the keys in 2^4 .. 2^5; of the values in 2^1 .. 2^9, so that most tiles have one power (or 1,
-  // where all are 0 or the smallest there is)
+  // values: their largest scale in 2^1 .. 2^9, so that most tiles have one power, or where that loses bits, as the keys, as high as it goes
   const int ek = exponent_of(top >> 16), ev = exponent_of(top & 0xFFFFu);
-  const int e[2] = {ek == kNone ? 0 : ek - 5, ev == kNone ? 0 : max(((ev - 2) >> 3) << 3, -24)};
+  int e[2] = {ek == kNone ? 0 : highest(ek), ev == kNone ? 0 : max(((ev - 2) >> 3) << 3, -24)};
+  if (ev != kNone && __syncthreads_or(lost_bits<C::SCALES>(d[1], scale_down<C::SCALES>(d[1], e[1])))) e[1] = highest(ev);
   const int64_t tile = (int64_t)blockIdx.y * a.tiles + blockIdx.x;
-  if (threadIdx.x == 0) a.units[tile] = (e[0] & 0xFFFF) | e[1] << 16;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const auto scales = scale_down<C::SCALES>(d[x], e[x]);
+    if (__any(lost_bits<C::SCALES>(d[x], scales))) s_lost = 1;
     u32x4* const dst = reinterpret_cast<u32x4*>((x ? a.values : a.keys) + (tile * kKeys + 16 * wave + row_in) * (32 * NB)) + NB * seg;
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
@@ -885,6 +1036,8 @@ __global__ __launch_bounds__(64 * kWaves) void attn_chunk_expand_kernel(ChunkArg
       dst[i] = x == 0 && out ? u32x4{~0u, ~0u, ~0u, ~0u} : y;
     }
   }
+  __syncthreads();
+  if (threadIdx.x == 0) a.units[tile] = (e[0] & 0xFF) | (s_lost ? kWide : 0) | (int)((uint32_t)e[1] << 16);
 }
 
 // Joins the parts of one row tile of a key head in their order: a workgroup takes 32 channels of its rows, so that a

@@ -604,7 +604,9 @@ nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v
  * Scores, softmax statistics and accumulation are float32; the probabilities enter the second product rounded
  * once to 16 bits (binary16 over Q8_0: 11 bits down to 2^-25 of the largest, as in nvq_attn_prompt).  Over
  * Q8_0 the operands are code * scale rounded to binary16 in a unit of their 64-key tile: 11 bits for blocks whose
- * scale is at least 2^-18 (keys) or 2^-15 (values) of the tile's largest, fewer below, none below 2^-28 and 2^-25;
+ * scale is at least 2^-22 (keys) or 2^-15 (values) of the tile's largest, fewer below, none below 2^-32 and 2^-25.
+ * That is for tiles that all queries of a row tile (128 rows of query and head) see whole; a tile that some of them do not, and
+ * that would lose bits so (values: from 2^-22 on), is computed in float32 from its codes, about 2 us a key slower.
  * bfloat16 queries' channels are held to 2^-32 of the largest.  Keys and values that a query does not see never
  * matter, whatever they hold.  An infinity or NaN in a value row shows, as one of them, in its channel (over
  * Q8_0 in its 32-channel block) of the queries that see it, in a key row in all of theirs.  out overlaps none of
