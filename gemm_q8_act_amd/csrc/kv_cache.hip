@@ -72,7 +72,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvArgs a) {
       for (int b = 0; b < NB; ++b) {
         const uint32_t u0 = __builtin_bit_cast(uint32_t, x[w][b][0]) & 0x7FFFFFFFu;
         const uint32_t u1 = __builtin_bit_cast(uint32_t, x[w][b][1]) & 0x7FFFFFFFu;
-        code[b] = quant_pair(x[w][b], row16_umax(max(u0, u1)), scale[b]);
+        code[b] = quant_pair(x[w][b], lanes_max<16>(max(u0, u1)), scale[b]);
       }
       if (row.cache >= 0) {
         store_halves<NB>(a.codes[w] + row.cache * (32 * NB) + 2 * NB * n, code);

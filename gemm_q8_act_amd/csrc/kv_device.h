@@ -6,12 +6,16 @@
 
 namespace nvq {
 
-// Largest of 16 lanes' unsigned values; magnitudes' bits order as their values do, infinity and NaN last
-__device__ __forceinline__ uint32_t row16_umax(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));
+// Largest of the unsigned values of a row's 16 or 8 lanes, the same in all of them; magnitudes' bits order as their values do,
+// infinity and NaN last
+template <int STEP>
+__device__ __forceinline__ uint32_t moved(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, STEP, 0xF, 0xF, true);
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  v = max(v, moved<0xB1>(v)), v = max(v, moved<0x4E>(v)), v = max(v, moved<0x141>(v));
+  if constexpr (LANES == 16) v = max(v, moved<0x140>(v));
   return v;
 }
 

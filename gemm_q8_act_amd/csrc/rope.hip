@@ -37,11 +37,7 @@ struct Args {
   int fmt;        // of the cache, -1: none
 };
 
-// Sum, and largest, over a row's lanes (16 or 8), the same in all of them.
-template <int STEP>
-__device__ __forceinline__ uint32_t moved(uint32_t x) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, STEP, 0xF, 0xF, true);
-}
+// Sum over a row's lanes (16 or 8), the same in all of them.
 template <int STEP>
 __device__ __forceinline__ float moved_f(float x) {
   return __builtin_bit_cast(float, moved<STEP>(__builtin_bit_cast(uint32_t, x)));
@@ -50,12 +46,6 @@ template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v) {
   v += moved_f<0xB1>(v), v += moved_f<0x4E>(v), v += moved_f<0x141>(v);
   if constexpr (LANES == 16) v += moved_f<0x140>(v);
-  return v;
-}
-template <int LANES>
-__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
-  v = max(v, moved<0xB1>(v)), v = max(v, moved<0x4E>(v)), v = max(v, moved<0x141>(v));
-  if constexpr (LANES == 16) v = max(v, moved<0x140>(v));
   return v;
 }
 
@@ -159,14 +149,10 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(Args a) {
     }
     const auto row_of = [&](int place, int c) __attribute__((always_inline)) { return r.table + ((uint32_t)place < (uint32_t)r.n_pos ? (int64_t)place * r.rot : 0) + c; };
     const auto angles = [&](const float* row, int b) __attribute__((always_inline)) {
-      if constexpr (EACH == 1) {
-        cos[b][0] = row[0], sin[b][0] = row[half];
-      } else {
 #pragma unroll
-        for (int i = 0; i < EACH; i += 2) {  // (half is even, and no more in general)
-          load_pair(row + i, reinterpret_cast<float(&)[2]>(cos[b][i]));
-          load_pair(row + half + i, reinterpret_cast<float(&)[2]>(sin[b][i]));
-        }
+      for (int i = 0; i < EACH; i += 2) {  // (half is even, and no more in general)
+        load_pair(row + i, reinterpret_cast<float(&)[2]>(cos[b][i]));
+        load_pair(row + half + i, reinterpret_cast<float(&)[2]>(sin[b][i]));
       }
     };
     // the first pair of block b that the lane turns
