@@ -784,7 +784,8 @@ def _rope_fine(table, positions, sections, T, q_weight, k_weight, D):
     axes = shape[0] if len(shape) == 2 else 1
     return (shape[-1] == T and (len(shape) == 2 or len(shape) == 1) and positions.dtype is _torch.int32 and positions.is_contiguous()
             and table.dtype is _torch.float32 and table.dim() == 2 and table.is_contiguous()
-            and (axes == 1 if sections is None else len(sections) == axes) and _weight_fine(q_weight, D) and _weight_fine(k_weight, D))
+            and (axes == 1 if sections is None else len(sections) == axes and (axes > 1 or 2 * sections[0] == table.shape[1]))
+            and _weight_fine(q_weight, D) and _weight_fine(k_weight, D))
 
 
 def _rope_here(table, positions, q_weight, k_weight, here):
@@ -802,6 +803,8 @@ def _wrong_rope(table, positions, sections, T, q_weight, k_weight, D):
     axes = positions.shape[0] if positions.dim() == 2 else 1
     if (axes != 1) if sections is None else len(sections) != axes:
         raise ValueError("sections: a number of pairs for each axis of positions is required")
+    if sections is not None and axes == 1 and 2 * sections[0] != table.shape[1]:
+        raise ValueError(f"sections: one axis turns all {table.shape[1] // 2} pairs")
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
             _wrong_dense(w, _torch.float32, (D,), name)
