@@ -30,11 +30,13 @@
 // in the prompt's kernel; the sum that divides them is of the rounded ones), results.
 //
 // What bounds it.  Many queries: the matrix and the vector unit in turn.  2048 queries (40 heads of 128 on 8) behind
-// 14336 keys in bfloat16 take 635 us, 1015 TFLOP/s, where a large matrix product reaches 1117; matrix
-// instructions are issued 47 % of the time, vector ones 37 %, no LDS conflicts.  Over Q8_0 715 us.  Heads of 64 have half
-// the products to the same softmax: 1024 queries, window of 4096, 59 us, 580 TFLOP/s.  Few queries: memory.  32 single
-// tokens behind 8000 keys each, bfloat16, 190 us (5.5 TB/s); a mixed batch of 24, 55 us.  The smallest calls are
-// latency: 16 tokens behind 484 keys 15 us in the two kernels.
+// 14336 keys in bfloat16 take 635 us, 1015 TFLOP/s; matrix
+// instructions are issued 50 % of the time, vector ones 40 %, no LDS conflicts.  Over Q8_0 715 to 740 us.  Heads of 64 have half
+// the products to the same softmax, and a wavefront's score products have no vector work beside them: 1024 queries, window of 4096, 59 us,
+// 580 TFLOP/s (matrix 25 %, vector 42 %).  Few queries: memory.  32 single
+// tokens behind 8000 keys each, bfloat16, 186 us (5.6 TB/s); over Q8_0 155 to 160 (3.6 TB/s: each tile is converted for 5 rows of 128).
+// A mixed batch of 24 (bfloat16): 49 to 55 us in 504 parts of up to 18 tiles.  The smallest calls are
+// latency: 16 tokens behind 484 keys 16 us in the two kernels.
 #include "attn_tiles.h"
 #include "nvq_launch.h"
 
@@ -56,7 +58,9 @@ constexpr int kOneRound = 128, kRounds = 2;
 // Q8_0 is turned into binary16 first from so many rows (query, head) a sequence on, on average, in so much workspace
 // at most: a tile is then converted once for all row tiles, and read from there in twice the bytes.  One sequence, 5
 // heads to a key head: 100 queries behind 32768 keys 112 us without and 142 with it, 205 behind 16000 122 and 122 (1025
-// rows), 512 of 16384 259 and 226, 2048 929 and 747.
+// rows), 512 of 16384 259 and 226, 2048 929 and 747.  The average is the batch's: 2048 queries with 23 single tokens behind 4000
+// keys each are not turned and take 218 us (92 and 100 in two calls), nor are 4096 beside 3 tokens behind 100000 keys, whose rows
+// would pass kExpandBytes, 905 us (238 and 190).
 constexpr int64_t kExpandRows = 8 * kRows, kExpandBytes = int64_t(1) << 30;
 // Workgroups that a call is planned for at once, for nb 32-blocks a row: about what registers hold to a compute unit.
 // Measured against one more: heads of 64, 1024 queries in a window 59 and 62 us; of 96, 512 queries of 4096 keys 51 and

@@ -580,7 +580,8 @@ nvq_status nvq_attn_decode_window(int fmt, int type, const void* q, int64_t q_st
  * out in no sequence are left alone; offsets outside the tensors are cut to them.  Scores,
  * softmax statistics and accumulation are float32; the probabilities enter the second product
  * rounded once to `type` (in binary16 to its 11 bits down to 2^-25 of the largest, with fewer down
- * to 2^-36, below that as 0).  Keys and values that a query does not see never matter, whatever they
+ * to 2^-36, below that as 0).  Scores (times log2 e) of 2^23 and more in binary16, about 2^31 in bfloat16, where float32 no
+ * longer holds their differences, can make a query's row NaN or 0.  Keys and values that a query does not see never matter, whatever they
  * hold (queries that an infinity or NaN in such a value row of their tile would reach are done
  * one by one, slowly: 8192 tokens with an infinite channel 115 ms for 0.63; rows of v that lie on one another, at a token stride below D, can give
  * NaN for an infinity then).  out overlaps none of the inputs. */
@@ -609,12 +610,14 @@ nvq_status nvq_attn_prompt(int type, const void* q, const void* k, const void* v
  * that would lose bits so (values: from 2^-22 on), is computed in float32 from its codes, about 2 us a key slower.
  * bfloat16 queries' channels are held to 2^-32 of the largest.  Keys and values that a query does not see never
  * matter, whatever they hold.  An infinity or NaN in a value row shows, as one of them, in its channel (over
- * Q8_0 in its 32-channel block) of the queries that see it, in a key row in all of theirs.  out overlaps none of
- * the inputs.
+ * Q8_0 in its 32-channel block) of the queries that see it, a NaN in a key row in all of theirs; an infinity there counts with the
+ * scores that it makes (over Q8_0 NaN).  out overlaps none of the inputs.
  * workspace: device, at least nvq_attn_chunk_workspace_bytes, contents irrelevant, overwritten; NULL when that
  * is 0.  Calls that share it must not overlap in time.  The bytes are those of a call's own shape: Q8_0 rows
  * are turned into binary16 there first, once for the call, where there are many queries to a sequence
- * (Tq * Hq/Hkv >= 1024 * B, B * Hkv < 65536, and up to 1 GiB of it), so that fewer of them, or more sequences, can need more or less. */
+ * (Tq * Hq/Hkv >= 1024 * B, B * Hkv < 65536, and up to 1 GiB of it), so that fewer of them, or more sequences, can need more or
+ * less.  That is one choice for the call, by the tables' width: a long piece of a prompt among many single tokens, or beside tokens behind
+ * very long prefixes, can be faster in a call of its own. */
 size_t nvq_attn_chunk_workspace_bytes(int fmt, int64_t B, int64_t Tq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_pages,
                                       int64_t page, int64_t window, int64_t sinks);
 nvq_status nvq_attn_chunk(int fmt, int type, const void* q, const int64_t* strides, int64_t B, int64_t Tq, int64_t Hq,
