@@ -58,3 +58,37 @@ def test_the_largest_score_takes_all(Hq, Hkv, D, seqs, window, sinks, scale, fmt
             assert np.isfinite(got[a:a + m]).all()
             a += m
         assert looked_at > a / 2
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (64, 2)])
+@pytest.mark.parametrize("type_", ["f16", "bf16"])
+def test_large_scores_beside_values_far_apart(type_, Hq, Hkv):
+    """The same over Q8_0 where the last key's values are 2^28 times the others', so that the last tile is computed by itself; its
+    largest scores come before, in, and behind that tile's.  (Other keys' probabilities are below e^-64: 2^28 times them is nothing.)"""
+    D, seqs = 64, [(70, 300), (60, 64)]
+    for size in SIZES[type_]:
+        r = np.random.Generator(np.random.PCG64(11))
+        kv, q = [], []
+        for m, n in seqs:
+            sign, c = r.choice([-1.0, 1.0], (1, Hkv, D)), 2.0 ** 15 * (1 + 2.0 ** -6) ** -r.permutation(1000)[:n]
+            v = r.standard_normal((n, Hkv, D)).astype(np.float32) * 1e-3
+            v[-1] *= 2.0 ** 28
+            kv.append(((c[:, None, None] * sign).astype(np.float32), v))
+            q.append(np.repeat(sign, Hq // Hkv, axis=1) * np.ones((m, 1, 1)) * size)
+        c = Paged("q8_0", kv, Hkv, D, 16, 5)
+        q = rounded(np.concatenate(q), type_)
+        got = host(call(c, on_gpu(q, type_), [m for m, _ in seqs], scale=1.0).float())
+        a = looked_at = 0
+        for i, (m, n) in enumerate(seqs):
+            seen = seen_of(m, n, 0, 0)
+            k, v = c.rows[i]
+            score = np.abs(k[:, 0, 0]).astype(np.float64) * size * D
+            for x in range(m - 1):
+                top = largest(np.where(seen[x], score, -np.inf))
+                if top is not None:
+                    want = v[top, np.arange(Hq) * Hkv // Hq]
+                    limit = (HALF_UNIT[type_] + 2.0 ** -11 + 2.0 ** -20) * 1.01 * np.abs(want) + 2.0 ** -24
+                    assert (np.abs(got[a + x] - want) <= limit).all(), f"sequence {i} query {x} size {size}"
+                    looked_at += 1
+            a += m
+        assert looked_at > a / 2
